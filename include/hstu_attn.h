@@ -104,6 +104,7 @@ typedef enum { HSTU_F32 = 0, HSTU_BF16 = 1 } hstu_dtype_t;
 #define HSTU_DEV_BAD_COUNTS    0x2   /* num_contextuals/num_targets negative or c + t > L */
 #define HSTU_DEV_SEQ_TOO_LONG  0x4   /* a sequence longer than max_seqlen */
 #define HSTU_DEV_WAIT_TIMEOUT  0x8   /* a bounded in-kernel wait gave up */
+#define HSTU_DEV_BAD_EXPERT    0x10  /* an expert id not below num_experts */
 
 typedef struct {
     int32_t batch;            /* B >= 0 */
@@ -324,6 +325,122 @@ hstu_status_t hstu_gather_rows(const void *src, int64_t row_bytes, const int64_t
 hstu_status_t hstu_jagged_concat(int32_t n_parts, const void *const *values,
                                  const int64_t *const *offsets, int32_t batch, int64_t row_bytes,
                                  void *out_values, int64_t *out_offsets, void *stream);
+
+/*
+ * Root-mean-square norm of rows with the residual's addition.
+ *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * weight
+ * x, residual (NULL: none), sum and y are [rows, width] of `dtype`, weight [width] fp32 (NULL:
+ * ones); width in 1..16384, rows <= 2^31 - 1.  The statistics and y come from the fp32 h; sum
+ * (NULL: not written; required when training with a residual) receives h rounded to dtype, and
+ * may be x or residual itself.  rstd [rows] fp32 (NULL: not written) is for the backward.
+ *
+ * hstu_rms_norm_rows_e4m3 writes y in 8 bits: q [rows, width] e4m3 (values up to 448, rounded to
+ * nearest even) and scales [rows, ceil(width / group)] fp32, group = 32, 64 or 128 columns per
+ * scale, or 0 for one scale per row: scale = max|y| / 448 over the group, y ~ q * scale.  A group
+ * of zeros has scale 0.  NaN stays NaN.
+ *
+ * hstu_rms_norm_rows_bwd: with xh = h * rstd and g = dy * weight, at the stored h,
+ *   dx = rstd * (g - xh * mean(g * xh)) + dsum;   dweight = sum over rows of dy * xh
+ * dx is the gradient of x and of residual alike; dsum (NULL: none) the gradient that reaches the
+ * sum by other ways.  dx may be dy or dsum itself.  dweight [width] fp32 (NULL: not computed)
+ * needs a workspace of hstu_rms_norm_rows_bwd_workspace_size bytes; the result does not depend on
+ * the order in which blocks run.
+ * Device pointers 16-byte aligned; each call enqueues kernels on `stream` and allocates nothing.
+ */
+hstu_status_t hstu_rms_norm_rows(const void *x, const void *residual, const float *weight,
+                                 int64_t rows, int32_t width, float eps, int32_t dtype, void *y,
+                                 void *sum, float *rstd, void *stream);
+hstu_status_t hstu_rms_norm_rows_e4m3(const void *x, const void *residual, const float *weight,
+                                      int64_t rows, int32_t width, float eps, int32_t dtype,
+                                      int32_t group, void *q, float *scales, void *sum,
+                                      float *rstd, void *stream);
+hstu_status_t hstu_rms_norm_rows_bwd_workspace_size(int64_t rows, int32_t width, size_t *bytes);
+hstu_status_t hstu_rms_norm_rows_bwd(const void *dy, const void *sum, const float *rstd,
+                                     const float *weight, const void *dsum, int64_t rows,
+                                     int32_t width, int32_t dtype, void *dx, float *dweight,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Mixture of experts on jagged rows.  tokens x choices pairs (token, expert) are sorted by
+ * expert; the sorted rows are a jagged tensor whose sequences are the experts.
+ *
+ * hstu_expert_sort: expert_ids [tokens, choices] (int32, or int64 when ids_64 = 1).  A negative
+ * id is a pair that no expert takes (padding); an id >= num_experts is treated the same and sets
+ * HSTU_DEV_BAD_EXPERT in *status (device int32, may be NULL).  Writes offsets [num_experts + 1]
+ * int64 (expert e's rows are offsets[e] .. offsets[e+1]-1), slots [tokens, choices] int32 (the
+ * pair's sorted row, -1 for pairs that no expert takes) and rows [tokens * choices] int64 (the
+ * token of each sorted row, as hstu_gather_rows takes it; NULL: not written; entries from
+ * offsets[num_experts] on are left as they were).  Within an expert, rows are in the order of
+ * the pairs.  num_experts in 1..1024, choices in 1..16, tokens * choices < 2^31.
+ *
+ * hstu_expert_dispatch: row t of x ([tokens] rows of row_bytes bytes, any type) to row slots[t, j]
+ * of out, for every j; with scales ([tokens, n_scales] fp32, NULL for none) their rows to
+ * scales_out alike.  Slots outside 0..max_rows-1 are skipped; rows of out that no slot names are
+ * left as they were.
+ *
+ * hstu_expert_combine: out_t = residual_t + sum over j of weights[t, j] * y[slots[t, j]], summed
+ * in fp32 in the order of j; y [max_rows, width], out and residual (NULL: none) [tokens, width] of
+ * `dtype`, weights [tokens, choices] fp32 (NULL: ones).  Without weights and residual it is the
+ * gradient of hstu_expert_dispatch.
+ *
+ * hstu_expert_combine_bwd: dy[slots[t, j]] = weights[t, j] * dout_t (rows of dy that no slot names
+ * are left as they were) and dweights[t, j] = <dout_t, y[slots[t, j]]> (0 for pairs without a
+ * row; NULL: not computed, and y may then be NULL).  The gradient of the residual is dout itself.
+ * A row of y belongs to one pair: slots that name a row twice leave that row of dy unspecified.
+ */
+hstu_status_t hstu_expert_sort_workspace_size(int64_t tokens, int32_t choices,
+                                              int32_t num_experts, size_t *bytes);
+hstu_status_t hstu_expert_sort(const void *expert_ids, int32_t ids_64, int64_t tokens,
+                               int32_t choices, int32_t num_experts, int32_t *slots,
+                               int64_t *offsets, int64_t *rows, int32_t *status, void *workspace,
+                               size_t workspace_bytes, void *stream);
+hstu_status_t hstu_expert_dispatch(const void *x, int64_t row_bytes, const float *scales,
+                                   int32_t n_scales, const int32_t *slots, int64_t tokens,
+                                   int32_t choices, int64_t max_rows, void *out,
+                                   float *scales_out, void *stream);
+hstu_status_t hstu_expert_combine(const void *y, const int32_t *slots, const float *weights,
+                                  const void *residual, int64_t tokens, int32_t choices,
+                                  int64_t max_rows, int32_t width, int32_t dtype, void *out,
+                                  void *stream);
+hstu_status_t hstu_expert_combine_bwd(const void *dout, const void *y, const int32_t *slots,
+                                      const float *weights, int64_t tokens, int32_t choices,
+                                      int64_t max_rows, int32_t width, int32_t dtype, void *dy,
+                                      float *dweights, void *stream);
+
+/*
+ * The experts' products: row s of expert e (offsets[e] <= s < offsets[e+1]) times that expert's
+ * matrix, on the tensor cores with fp32 accumulation.  offsets [num_experts + 1] int64 are read on
+ * the device; an expert whose offsets are not 0 <= offsets[e] <= offsets[e+1] <= rows has no rows
+ * and sets HSTU_DEV_BAD_OFFSETS in *status (device int32, may be NULL, not cleared here).  Output
+ * rows of no expert are left as they were.  Where offsets make experts overlap, their rows are
+ * unspecified.
+ *
+ * hstu_expert_proj: out [rows, d_out] = x [rows, d_in] w[e], w [num_experts, d_in, d_out], bf16;
+ * silu = 1 writes SiLU of the product, and then the product itself to pre when that is not NULL.
+ * d_in and d_out multiples of 8.
+ *
+ * hstu_expert_proj_e4m3: out [rows, d_out] (bf16) of e4m3 x [rows, d_in] with scales [rows] and
+ * e4m3 w [num_experts, d_out, d_in] (rows along d_in) with scales [num_experts, d_out]:
+ * out = x_scales[s] * w_scales[e, o] * sum_i x[s, i] w[e, o, i], then SiLU when silu = 1.
+ * d_in a multiple of 16, d_out of 8.
+ *
+ * hstu_expert_proj_bwd: the gradients of hstu_expert_proj's product.  dx [rows, d_in] = dout w[e]^T
+ * (NULL: not computed); with silu_pre [rows, d_in] (NULL for none) times SiLU'(silu_pre), the
+ * gradient ahead of the SiLU that made x.  dw [num_experts, d_in, d_out] = sum over the expert's
+ * rows of x_s^T dout_s (NULL: not computed; zeros for an expert without rows).  bf16.
+ * Device pointers 16-byte aligned; each call enqueues kernels on `stream` and allocates nothing.
+ */
+hstu_status_t hstu_expert_proj(const void *x, const void *w, const int64_t *offsets, int64_t rows,
+                               int32_t num_experts, int32_t d_in, int32_t d_out, int32_t silu,
+                               void *out, void *pre, int32_t *status, void *stream);
+hstu_status_t hstu_expert_proj_e4m3(const void *x, const float *x_scales, const void *w,
+                                    const float *w_scales, const int64_t *offsets, int64_t rows,
+                                    int32_t num_experts, int32_t d_in, int32_t d_out,
+                                    int32_t silu, void *out, int32_t *status, void *stream);
+hstu_status_t hstu_expert_proj_bwd(const void *dout, const void *x, const void *w,
+                                   const int64_t *offsets, const void *silu_pre, int64_t rows,
+                                   int32_t num_experts, int32_t d_in, int32_t d_out, void *dx,
+                                   void *dw, int32_t *status, void *stream);
 
 /* Static description of a status code. */
 const char *hstu_status_string(hstu_status_t status);

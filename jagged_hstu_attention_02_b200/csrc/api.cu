@@ -3,12 +3,14 @@
 // caller's stream.  Allocates nothing and never synchronises in fwd/bwd.
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <utility>
 #include <vector>
 
 #include "common.cuh"
+#include "experts.h"
 #include "kernels.h"
 #include "sm100.cuh"
 
@@ -174,6 +176,66 @@ struct StageScope {
         cudaError_t err_ = (expr);                            \
         if (err_ != cudaSuccess) return HSTU_ERR_CUDA;        \
     } while (0)
+
+bool all_aligned16(std::initializer_list<const void *> ptrs)
+{
+    for (const void *x : ptrs)
+        if (!aligned16(x)) return false;
+    return true;
+}
+
+bool dtype_ok(int32_t dtype) { return dtype == HSTU_F32 || dtype == HSTU_BF16; }
+
+bool rms_shape_ok(int64_t rows, int32_t width)
+{
+    return rows >= 0 && rows <= INT32_MAX && width >= 1 && width <= kMaxNormWidth;
+}
+
+hstu_status_t rms_norm(const void *x, const void *residual, const float *weight, int64_t rows,
+                       int32_t width, float eps, int32_t dtype, int32_t group, void *y,
+                       float *scales, void *sum, float *rstd, bool e4m3, void *stream)
+{
+    if (!rms_shape_ok(rows, width) || !dtype_ok(dtype) || !(eps >= 0.f) || !std::isfinite(eps) ||
+        (rows > 0 && (!x || !y || (e4m3 && !scales))))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (!all_aligned16({x, residual, weight, y, scales, sum, rstd}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    RmsArgs a = {x, residual, weight, rows, width, eps, group, y, sum, scales, rstd};
+    return launch_rms_norm(a, dtype == HSTU_F32, e4m3, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? HSTU_OK
+               : HSTU_ERR_CUDA;
+}
+
+bool route_shape_ok(int64_t tokens, int32_t choices)
+{
+    return tokens >= 0 && choices >= 1 && choices <= kMaxChoices &&
+           tokens <= INT32_MAX / choices;
+}
+
+bool proj_shape_ok(int64_t rows, int32_t experts, int32_t d_in, int32_t d_out, int32_t in_step)
+{
+    return rows >= 0 && rows <= INT32_MAX && experts >= 1 && experts <= kMaxExperts && d_in >= 1 &&
+           d_in % in_step == 0 && d_in <= 65536 && d_out >= 1 && d_out % 8 == 0 && d_out <= 65536;
+}
+
+ProjArgs proj_args(const void *x, const void *w, const int64_t *offsets, int64_t rows,
+                   int32_t experts, int32_t d_in, int32_t d_out, int32_t *status)
+{
+    ProjArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.w = w;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.experts = experts;
+    a.k = d_in;
+    a.n = d_out;
+    a.status = status;
+    a.wait_limit = g_wait_limit;
+    a.stall_test = g_stall_test;
+    return a;
+}
 
 }  // namespace
 
@@ -521,6 +583,188 @@ hstu_status_t hstu_jagged_concat(int32_t n_parts, const void *const *values,
         if (!values[q] || !offsets[q]) return HSTU_ERR_INVALID_ARGUMENT;
     HSTU_CUDA_TRY(launch_jagged_concat(n_parts, values, offsets, batch, row_bytes, out_values,
                                        out_offsets, reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_rms_norm_rows_bwd_workspace_size(int64_t rows, int32_t width, size_t *bytes)
+{
+    if (!bytes || !rms_shape_ok(rows, width)) return HSTU_ERR_INVALID_ARGUMENT;
+    *bytes = (size_t)rms_bwd_blocks(rows, width) * (size_t)align_up(width, 4) * 4;
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_rms_norm_rows(const void *x, const void *residual, const float *weight,
+                                 int64_t rows, int32_t width, float eps, int32_t dtype, void *y,
+                                 void *sum, float *rstd, void *stream)
+{
+    return rms_norm(x, residual, weight, rows, width, eps, dtype, 0, y, nullptr, sum, rstd, false,
+                    stream);
+}
+
+hstu_status_t hstu_rms_norm_rows_e4m3(const void *x, const void *residual, const float *weight,
+                                      int64_t rows, int32_t width, float eps, int32_t dtype,
+                                      int32_t group, void *q, float *scales, void *sum,
+                                      float *rstd, void *stream)
+{
+    if (group != 0 && group != 32 && group != 64 && group != 128) return HSTU_ERR_INVALID_ARGUMENT;
+    return rms_norm(x, residual, weight, rows, width, eps, dtype, group, q, scales, sum, rstd,
+                    true, stream);
+}
+
+hstu_status_t hstu_rms_norm_rows_bwd(const void *dy, const void *sum, const float *rstd,
+                                     const float *weight, const void *dsum, int64_t rows,
+                                     int32_t width, int32_t dtype, void *dx, float *dweight,
+                                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!rms_shape_ok(rows, width) || !dtype_ok(dtype) ||
+        (rows > 0 && (!dy || !sum || !rstd || !dx)) || (rows > 0 && dweight && !workspace))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (!all_aligned16({dy, sum, rstd, weight, dsum, dx, dweight, workspace}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    size_t need = 0;
+    if (rows > 0 && dweight) hstu_rms_norm_rows_bwd_workspace_size(rows, width, &need);
+    if (workspace_bytes < need) return HSTU_ERR_WORKSPACE_TOO_SMALL;
+    RmsBwdArgs a = {dy, sum, dsum, rstd, weight, rows, width, dx, dweight,
+                    reinterpret_cast<float *>(workspace)};
+    HSTU_CUDA_TRY(launch_rms_norm_bwd(a, dtype == HSTU_F32, reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_sort_workspace_size(int64_t tokens, int32_t choices,
+                                              int32_t num_experts, size_t *bytes)
+{
+    if (!bytes || !route_shape_ok(tokens, choices) || num_experts < 1 || num_experts > kMaxExperts)
+        return HSTU_ERR_INVALID_ARGUMENT;
+    const int blocks = sort_blocks(tokens * choices);
+    *bytes = blocks > 1 ? (size_t)blocks * num_experts * 4 : 0;
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_sort(const void *expert_ids, int32_t ids_64, int64_t tokens,
+                               int32_t choices, int32_t num_experts, int32_t *slots,
+                               int64_t *offsets, int64_t *rows, int32_t *status, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    size_t need = 0;
+    hstu_status_t st = hstu_expert_sort_workspace_size(tokens, choices, num_experts, &need);
+    if (st != HSTU_OK) return st;
+    if ((ids_64 != 0 && ids_64 != 1) || !offsets || (tokens > 0 && (!expert_ids || !slots)) ||
+        (need > 0 && !workspace) ||
+        !all_aligned16({expert_ids, slots, offsets, rows, workspace}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return HSTU_ERR_WORKSPACE_TOO_SMALL;
+    SortArgs a = {expert_ids, tokens * choices, choices, num_experts, slots, offsets, rows, status,
+                  reinterpret_cast<int32_t *>(workspace)};
+    HSTU_CUDA_TRY(launch_expert_sort(a, ids_64 != 0, reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_dispatch(const void *x, int64_t row_bytes, const float *scales,
+                                   int32_t n_scales, const int32_t *slots, int64_t tokens,
+                                   int32_t choices, int64_t max_rows, void *out,
+                                   float *scales_out, void *stream)
+{
+    if (!route_shape_ok(tokens, choices) || row_bytes < 1 || row_bytes > ((int64_t)1 << 31) ||
+        max_rows < 0 || (scales && n_scales < 1) || (scales != nullptr) != (scales_out != nullptr))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (tokens == 0 || max_rows == 0) return HSTU_OK;
+    if (!x || !slots || !out || !all_aligned16({x, slots, out, scales, scales_out}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    DispatchArgs a = {reinterpret_cast<const uint8_t *>(x), scales, slots, tokens, row_bytes,
+                      max_rows, choices, n_scales, reinterpret_cast<uint8_t *>(out), scales_out};
+    HSTU_CUDA_TRY(launch_expert_dispatch(a, reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_combine(const void *y, const int32_t *slots, const float *weights,
+                                  const void *residual, int64_t tokens, int32_t choices,
+                                  int64_t max_rows, int32_t width, int32_t dtype, void *out,
+                                  void *stream)
+{
+    if (!route_shape_ok(tokens, choices) || max_rows < 0 || width < 1 || !dtype_ok(dtype))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (tokens == 0) return HSTU_OK;
+    if ((max_rows > 0 && !y) || !slots || !out ||
+        !all_aligned16({y, slots, weights, residual, out}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    CombineArgs a = {y, slots, weights, residual, nullptr, tokens, max_rows, choices, width, out,
+                     nullptr, nullptr};
+    HSTU_CUDA_TRY(launch_expert_combine(a, dtype == HSTU_F32, reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_combine_bwd(const void *dout, const void *y, const int32_t *slots,
+                                      const float *weights, int64_t tokens, int32_t choices,
+                                      int64_t max_rows, int32_t width, int32_t dtype, void *dy,
+                                      float *dweights, void *stream)
+{
+    if (!route_shape_ok(tokens, choices) || max_rows < 0 || width < 1 || !dtype_ok(dtype))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (tokens == 0) return HSTU_OK;
+    if (!dout || !slots || (max_rows > 0 && (!dy || (dweights && !y))) ||
+        !all_aligned16({dout, y, slots, weights, dy, dweights}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    CombineArgs a = {y, slots, weights, nullptr, dout, tokens, max_rows, choices, width, nullptr,
+                     dy, dweights};
+    HSTU_CUDA_TRY(launch_expert_combine_bwd(a, dtype == HSTU_F32,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_proj(const void *x, const void *w, const int64_t *offsets, int64_t rows,
+                               int32_t num_experts, int32_t d_in, int32_t d_out, int32_t silu,
+                               void *out, void *pre, int32_t *status, void *stream)
+{
+    if (!proj_shape_ok(rows, num_experts, d_in, d_out, 8) || (silu != 0 && silu != 1) ||
+        (pre && !silu))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return HSTU_OK;
+    if (!x || !w || !offsets || !out || !all_aligned16({x, w, offsets, out, pre}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    ProjArgs a = proj_args(x, w, offsets, rows, num_experts, d_in, d_out, status);
+    a.silu = silu;
+    a.out = out;
+    a.pre = pre;
+    HSTU_CUDA_TRY(launch_expert_proj(a, false, reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_proj_e4m3(const void *x, const float *x_scales, const void *w,
+                                    const float *w_scales, const int64_t *offsets, int64_t rows,
+                                    int32_t num_experts, int32_t d_in, int32_t d_out,
+                                    int32_t silu, void *out, int32_t *status, void *stream)
+{
+    if (!proj_shape_ok(rows, num_experts, d_in, d_out, 16) || (silu != 0 && silu != 1))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return HSTU_OK;
+    if (!x || !x_scales || !w || !w_scales || !offsets || !out ||
+        !all_aligned16({x, x_scales, w, w_scales, offsets, out}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    ProjArgs a = proj_args(x, w, offsets, rows, num_experts, d_in, d_out, status);
+    a.x_scales = x_scales;
+    a.w_scales = w_scales;
+    a.silu = silu;
+    a.out = out;
+    HSTU_CUDA_TRY(launch_expert_proj(a, true, reinterpret_cast<cudaStream_t>(stream)));
+    return HSTU_OK;
+}
+
+hstu_status_t hstu_expert_proj_bwd(const void *dout, const void *x, const void *w,
+                                   const int64_t *offsets, const void *silu_pre, int64_t rows,
+                                   int32_t num_experts, int32_t d_in, int32_t d_out, void *dx,
+                                   void *dw, int32_t *status, void *stream)
+{
+    if (!proj_shape_ok(rows, num_experts, d_in, d_out, 8)) return HSTU_ERR_INVALID_ARGUMENT;
+    if (!offsets || (rows > 0 && (!dout || (dx && !w) || (dw && !x))) ||
+        !all_aligned16({dout, x, w, offsets, silu_pre, dx, dw}))
+        return HSTU_ERR_INVALID_ARGUMENT;
+    ProjArgs a = proj_args(x, w, offsets, rows, num_experts, d_in, d_out, status);
+    a.dout = dout;
+    a.silu_pre = silu_pre;
+    a.dx = dx;
+    a.dw = dw;
+    if (dx) HSTU_CUDA_TRY(launch_expert_proj_dx(a, reinterpret_cast<cudaStream_t>(stream)));
+    if (dw) HSTU_CUDA_TRY(launch_expert_proj_dw(a, reinterpret_cast<cudaStream_t>(stream)));
     return HSTU_OK;
 }
 

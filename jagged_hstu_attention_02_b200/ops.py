@@ -6,10 +6,11 @@ path: without the built library, or with tensors not on a CUDA device, calls rai
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 import torch
@@ -21,12 +22,18 @@ HSTU_F32, HSTU_BF16 = 0, 1
 STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small",
                 4: "CUDA error", 5: "invalid device data"}
 DEV_BAD_OFFSETS, DEV_BAD_COUNTS, DEV_SEQ_TOO_LONG, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_EXPERT = 0x10
 
 EXPORTED = ["hstu_attn_fwd_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd_workspace_size",
             "hstu_attn_bwd", "hstu_attn_read_device_status", "hstu_attn_debug_mask",
             "hstu_attn_debug_kernel_mask", "hstu_attn_set_wait_test",
             "hstu_stochastic_length", "hstu_gather_rows", "hstu_jagged_concat",
             "hstu_layer_norm_rows", "hstu_uvqk_proj", "hstu_out_proj",
+            "hstu_rms_norm_rows", "hstu_rms_norm_rows_e4m3",
+            "hstu_rms_norm_rows_bwd_workspace_size", "hstu_rms_norm_rows_bwd",
+            "hstu_expert_sort_workspace_size", "hstu_expert_sort", "hstu_expert_dispatch",
+            "hstu_expert_combine", "hstu_expert_combine_bwd", "hstu_expert_proj",
+            "hstu_expert_proj_e4m3", "hstu_expert_proj_bwd",
             "hstu_attn_time_thresholds", "hstu_attn_set_stage_events", "hstu_status_string",
             "hstu_attn_version"]
 STAGES = {"fwd_attn": 0, "fwd_norm": 1, "bwd_norm": 2, "bwd_attn": 3}
@@ -90,6 +97,21 @@ def lib():
         L.hstu_jagged_concat.argtypes = [ctypes.c_int32, ctypes.POINTER(_VP),
                                          ctypes.POINTER(_VP), ctypes.c_int32, ctypes.c_int64,
                                          _VP, _VP, _VP]
+        i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        L.hstu_rms_norm_rows.argtypes = [_VP] * 3 + [i64, i32, f32, i32] + [_VP] * 4
+        L.hstu_rms_norm_rows_e4m3.argtypes = [_VP] * 3 + [i64, i32, f32, i32, i32] + [_VP] * 5
+        L.hstu_rms_norm_rows_bwd_workspace_size.argtypes = [i64, i32, sz]
+        L.hstu_rms_norm_rows_bwd.argtypes = [_VP] * 5 + [i64, i32, i32] + [_VP] * 3 + [
+            ctypes.c_size_t, _VP]
+        L.hstu_expert_sort_workspace_size.argtypes = [i64, i32, i32, sz]
+        L.hstu_expert_sort.argtypes = [_VP, i32, i64, i32, i32] + [_VP] * 5 + [ctypes.c_size_t,
+                                                                              _VP]
+        L.hstu_expert_dispatch.argtypes = [_VP, i64, _VP, i32, _VP, i64, i32, i64] + [_VP] * 3
+        L.hstu_expert_combine.argtypes = [_VP] * 4 + [i64, i32, i64, i32, i32] + [_VP] * 2
+        L.hstu_expert_combine_bwd.argtypes = [_VP] * 4 + [i64, i32, i64, i32, i32] + [_VP] * 3
+        L.hstu_expert_proj.argtypes = [_VP] * 3 + [i64, i32, i32, i32, i32] + [_VP] * 4
+        L.hstu_expert_proj_e4m3.argtypes = [_VP] * 5 + [i64, i32, i32, i32, i32] + [_VP] * 3
+        L.hstu_expert_proj_bwd.argtypes = [_VP] * 5 + [i64, i32, i32, i32] + [_VP] * 4
         L.hstu_status_string.restype = ctypes.c_char_p
         L.hstu_status_string.argtypes = [ctypes.c_int]
         L.hstu_attn_version.restype = ctypes.c_int32
@@ -377,6 +399,387 @@ def layer_fwd(x, seq_offsets, num_contextuals, num_targets, timestamps, rel_bias
                stream=stream)
     o = out_proj(attn, w_o, b_o, x, stream=stream)
     return dict(xn=xn, u=u, v=v, q=q, k=k, attn=attn, o=o)
+
+
+# ------------------------------------------------------------------ mixture of experts
+
+F8 = torch.float8_e4m3fn
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Where a call allocates and launches: the tensors' device, and `stream` (of that device)
+    or that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream and tensors must be on the same device")
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return _HERE
+    return torch.cuda.device(device)
+
+
+def _expect(t, name, dtype, shape, like=None):
+    """Checks an optional tensor's type, shape and (like: a tensor) device."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if like is not None and t.device != like.device:
+        raise ValueError("%s must be on %s" % (name, like.device))
+
+
+def _expect_slots(slots, like, name="slots"):
+    if slots.dim() != 2:
+        raise ValueError("%s must be [tokens, choices]" % name)
+    _expect(slots, name, torch.int32, slots.shape, like)
+    return slots.shape
+
+
+def _expect_status(status, like):
+    if status is not None:
+        _expect(status.reshape(-1)[:1], "status", torch.int32, (1,), like)
+
+
+class RmsNorm(NamedTuple):
+    """Results of rms_norm_rows: y (e4m3 with scales, or the rows' type), the stored sum (x
+    itself without a residual) and, when training, rstd."""
+    y: torch.Tensor
+    scales: Optional[torch.Tensor]
+    sum: torch.Tensor
+    rstd: Optional[torch.Tensor]
+
+
+def rms_norm_rows(x, weight=None, residual=None, *, eps=1e-5, e4m3=False, group=0,
+                  training=False, out: Optional[RmsNorm] = None, stream=None) -> RmsNorm:
+    """RMS norm of the rows of h = x (+ residual), times weight (fp32).  e4m3: y in 8 bits with
+    one fp32 scale per row (group 0) or per `group` (32, 64, 128) columns, y ~ q * scale.
+    training keeps rstd for rms_norm_rows_bwd.  out: a result to write into again."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, width]")
+    rows, width = x.shape
+    code = dtype_code(x)
+    if group not in (0, 32, 64, 128):
+        raise ValueError("group must be 0, 32, 64 or 128")
+    if group and not e4m3:
+        raise ValueError("group is for the e4m3 output")
+    _expect(weight, "weight", torch.float32, (width,), x)
+    _expect(residual, "residual", x.dtype, x.shape, x)
+    groups = -(-width // group) if group else 1
+    with _on(x.device, stream):
+        if out is None:
+            dev = x.device
+            out = RmsNorm(torch.empty_like(x, dtype=F8 if e4m3 else x.dtype),
+                          torch.empty((rows, groups), dtype=torch.float32, device=dev)
+                          if e4m3 else None,
+                          torch.empty_like(x) if residual is not None else x,
+                          torch.empty(rows, dtype=torch.float32, device=dev)
+                          if training else None)
+        else:
+            _expect(out.y, "out.y", F8 if e4m3 else x.dtype, x.shape, x)
+            _expect(out.scales, "out.scales", torch.float32, (rows, groups), x)
+            _expect(out.sum, "out.sum", x.dtype, x.shape, x)
+            _expect(out.rstd, "out.rstd", torch.float32, (rows,), x)
+            if (e4m3 and out.scales is None) or (training and out.rstd is None):
+                raise ValueError("out lacks scales or rstd")
+        keep = out.sum if residual is not None else None
+        if e4m3:
+            st = lib().hstu_rms_norm_rows_e4m3(
+                _ptr(x), _ptr(residual), _ptr(weight), rows, width, eps, code, group, _ptr(out.y),
+                _ptr(out.scales), _ptr(keep), _ptr(out.rstd), _stream(None))
+        else:
+            st = lib().hstu_rms_norm_rows(
+                _ptr(x), _ptr(residual), _ptr(weight), rows, width, eps, code, _ptr(out.y),
+                _ptr(keep), _ptr(out.rstd), _stream(None))
+    _check(st, "hstu_rms_norm_rows")
+    return out
+
+
+def rms_norm_rows_bwd(dy, sum, rstd, weight=None, *, dsum=None, grads=None, workspace=None,
+                      stream=None):
+    """(dx, dweight or None) of rms_norm_rows at its stored sum; dx is the gradient of x and of
+    the residual, dsum the gradient that reaches the sum by other ways."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be [rows, width]")
+    rows, width = dy.shape
+    code = dtype_code(dy)
+    _expect(sum, "sum", dy.dtype, dy.shape, dy)
+    _expect(rstd, "rstd", torch.float32, (rows,), dy)
+    _expect(weight, "weight", torch.float32, (width,), dy)
+    _expect(dsum, "dsum", dy.dtype, dy.shape, dy)
+    with _on(dy.device, stream):
+        if grads is None:
+            grads = (torch.empty_like(dy), None if weight is None else torch.empty_like(weight))
+        dx, dw = grads
+        _expect(dx, "dx", dy.dtype, dy.shape, dy)
+        _expect(dw, "dweight", torch.float32, (width,), dy)
+        if dw is not None and workspace is None:
+            n = ctypes.c_size_t()
+            _check(lib().hstu_rms_norm_rows_bwd_workspace_size(rows, width, ctypes.byref(n)),
+                   "hstu_rms_norm_rows_bwd_workspace_size")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dy.device)
+        st = lib().hstu_rms_norm_rows_bwd(
+            _ptr(dy), _ptr(sum), _ptr(rstd), _ptr(weight), _ptr(dsum), rows, width, code, _ptr(dx),
+            _ptr(dw), _ptr(workspace), _bytes(workspace), _stream(None))
+    _check(st, "hstu_rms_norm_rows_bwd")
+    return grads
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+class Routing(NamedTuple):
+    """Where expert_sort puts the pairs: slots [tokens, choices] (the pair's sorted row, -1 for
+    none), offsets [experts + 1] of the sorted rows, rows [tokens * choices] (each sorted row's
+    token, as gather_rows takes them; offsets[-1] of them)."""
+    slots: torch.Tensor
+    offsets: torch.Tensor
+    rows: Optional[torch.Tensor]
+
+
+def expert_sort(expert_ids, num_experts: int, *, status=None, out: Optional[Routing] = None,
+                workspace=None, stream=None) -> Routing:
+    """Sorts the pairs of expert_ids [tokens, choices] (int32 or int64; negative: no expert) by
+    expert, in the order of the pairs within an expert."""
+    if expert_ids.dim() != 2:
+        raise ValueError("expert_ids must be [tokens, choices]")
+    if expert_ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("expert_ids must be int32 or int64")
+    T, k = expert_ids.shape
+    _expect_status(status, expert_ids)
+    with _on(expert_ids.device, stream):
+        dev = expert_ids.device
+        if out is None:
+            out = Routing(torch.empty((T, k), dtype=torch.int32, device=dev),
+                          torch.empty(num_experts + 1, dtype=torch.int64, device=dev),
+                          torch.empty(T * k, dtype=torch.int64, device=dev))
+        else:
+            _expect(out.slots, "out.slots", torch.int32, (T, k), expert_ids)
+            _expect(out.offsets, "out.offsets", torch.int64, (num_experts + 1,), expert_ids)
+            _expect(out.rows, "out.rows", torch.int64, (T * k,), expert_ids)
+        if workspace is None:
+            n = ctypes.c_size_t()
+            _check(lib().hstu_expert_sort_workspace_size(T, k, num_experts, ctypes.byref(n)),
+                   "hstu_expert_sort_workspace_size")
+            if n.value:
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        st = lib().hstu_expert_sort(
+            _ptr(expert_ids), 1 if expert_ids.dtype == torch.int64 else 0, T, k, num_experts,
+            _ptr(out.slots), _ptr(out.offsets), _ptr(out.rows), _ptr(status), _ptr(workspace),
+            _bytes(workspace), _stream(None))
+    _check(st, "hstu_expert_sort")
+    return out
+
+
+def expert_dispatch(x, slots, *, scales=None, out=None, scales_out=None, stream=None):
+    """xs [tokens * choices, ...]: row t of x at every slots[t, j]; with scales (one row of fp32
+    per token, e.g. of e4m3 rows) (xs, their scales).  Rows that no slot names are left as they
+    were in out."""
+    T, k = _expect_slots(slots, x)
+    if x.dim() < 2 or x.shape[0] != T:
+        raise ValueError("x must be [tokens, ...] with the slots' tokens")
+    if (scales_out is not None) and scales is None:
+        raise ValueError("scales_out without scales")
+    if scales is not None:
+        if scales.dim() != 2:
+            raise ValueError("scales must be [tokens, n]")
+        _expect(scales, "scales", torch.float32, (T, scales.shape[1]), x)
+    row = x.shape[1:].numel()
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty((T * k,) + tuple(x.shape[1:]), dtype=x.dtype, device=x.device)
+        elif out.dim() < 1 or out.shape[1:] != x.shape[1:]:
+            raise ValueError("out must have rows like x")
+        _expect(out, "out", x.dtype, out.shape, x)
+        if scales is not None:
+            if scales_out is None:
+                scales_out = torch.empty((out.shape[0], scales.shape[1]), dtype=torch.float32,
+                                         device=x.device)
+            _expect(scales_out, "scales_out", torch.float32, (out.shape[0], scales.shape[1]), x)
+        if row:
+            st = lib().hstu_expert_dispatch(
+                _ptr(x), row * x.element_size(), _ptr(scales),
+                0 if scales is None else scales.shape[1], _ptr(slots), T, k, out.shape[0],
+                _ptr(out), _ptr(scales_out), _stream(None))
+            _check(st, "hstu_expert_dispatch")
+    return out if scales is None else (out, scales_out)
+
+
+def expert_combine(y, slots, weights=None, *, residual=None, out=None, stream=None):
+    """out [tokens, width] = residual + sum over j of weights[:, j] * y[slots[:, j]]."""
+    T, k = _expect_slots(slots, y)
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, width]")
+    shape = (T, y.shape[1])
+    code = dtype_code(y)
+    _expect(weights, "weights", torch.float32, (T, k), y)
+    _expect(residual, "residual", y.dtype, shape, y)
+    _expect(out, "out", y.dtype, shape, y)
+    with _on(y.device, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=y.dtype, device=y.device)
+        st = lib().hstu_expert_combine(
+            _ptr(y), _ptr(slots), _ptr(weights), _ptr(residual), T, k, y.shape[0], y.shape[1],
+            code, _ptr(out), _stream(None))
+    _check(st, "hstu_expert_combine")
+    return out
+
+
+def expert_combine_bwd(dout, y, slots, weights=None, *, grads=None, stream=None):
+    """(dy, dweights or None) of expert_combine; rows of dy that no slot names are left as they
+    were.  The residual's gradient is dout itself."""
+    T, k = _expect_slots(slots, y)
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, width]")
+    code = dtype_code(y)
+    _expect(dout, "dout", y.dtype, (T, y.shape[1]), y)
+    _expect(weights, "weights", torch.float32, (T, k), y)
+    with _on(y.device, stream):
+        if grads is None:
+            grads = (torch.empty_like(y), None if weights is None else torch.empty_like(weights))
+        dy, dw = grads
+        _expect(dy, "dy", y.dtype, y.shape, y)
+        _expect(dw, "dweights", torch.float32, (T, k), y)
+        st = lib().hstu_expert_combine_bwd(
+            _ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, y.shape[0], y.shape[1], code,
+            _ptr(dy), _ptr(dw), _stream(None))
+    _check(st, "hstu_expert_combine_bwd")
+    return grads
+
+
+def expert_dispatch_bwd(dxs, slots, *, out=None, stream=None):
+    """dx [tokens, width] of expert_dispatch: each token's sum over its sorted rows."""
+    return expert_combine(dxs, slots, out=out, stream=stream)
+
+
+def _expect_experts(offsets, experts, like):
+    _expect(offsets, "offsets", torch.int64, (experts + 1,), like)
+
+
+def expert_proj(x, w, offsets, *, silu=False, pre=None, out=None, status=None, stream=None):
+    """out [rows, d_out]: each expert's rows offsets[e] .. offsets[e+1] of x [rows, d_in] (bf16)
+    times w[e] of [experts, d_in, d_out], SiLU after it when silu (the product itself then to
+    pre, when given).  Rows of no expert are left as they were in out."""
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, d_in] and w [experts, d_in, d_out]")
+    S, K = x.shape
+    E, N = w.shape[0], w.shape[2]
+    _expect(x, "x", torch.bfloat16, (S, K))
+    _expect(w, "w", torch.bfloat16, (E, K, N), x)
+    _expect_experts(offsets, E, x)
+    _expect(pre, "pre", torch.bfloat16, (S, N), x)
+    _expect(out, "out", torch.bfloat16, (S, N), x)
+    _expect_status(status, x)
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
+        st = lib().hstu_expert_proj(_ptr(x), _ptr(w), _ptr(offsets), S, E, K, N,
+                                    1 if silu else 0, _ptr(out), _ptr(pre), _ptr(status),
+                                    _stream(None))
+    _check(st, "hstu_expert_proj")
+    return out
+
+
+def expert_proj_e4m3(x, x_scales, w, w_scales, offsets, *, silu=False, out=None, status=None,
+                     stream=None):
+    """expert_proj of e4m3 rows x [rows, d_in] with scales (one fp32 per row) and e4m3 weights w
+    [experts, d_out, d_in] with scales [experts, d_out]; out is bf16."""
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, d_in] and w [experts, d_out, d_in]")
+    S, K = x.shape
+    E, N = w.shape[0], w.shape[1]
+    _expect(x, "x", F8, (S, K))
+    _expect(w, "w", F8, (E, N, K), x)
+    _expect(x_scales, "x_scales", torch.float32,
+            (S, 1) if x_scales.dim() == 2 else (S,), x)
+    _expect(w_scales, "w_scales", torch.float32, (E, N), x)
+    _expect_experts(offsets, E, x)
+    _expect(out, "out", torch.bfloat16, (S, N), x)
+    _expect_status(status, x)
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
+        st = lib().hstu_expert_proj_e4m3(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales),
+                                         _ptr(offsets), S, E, K, N, 1 if silu else 0, _ptr(out),
+                                         _ptr(status), _stream(None))
+    _check(st, "hstu_expert_proj_e4m3")
+    return out
+
+
+def expert_proj_bwd(dout, x, w, offsets, *, silu_pre=None, grads=None, status=None, stream=None):
+    """(dx, dw) of expert_proj's product.  With silu_pre (x = SiLU(silu_pre)), dx is the gradient
+    of silu_pre.  grads: (dx, dw) to write into, None in the place of one not wanted; rows of dx
+    of no expert are left as they were."""
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, d_in] and w [experts, d_in, d_out]")
+    S, K = x.shape
+    E, N = w.shape[0], w.shape[2]
+    _expect(x, "x", torch.bfloat16, (S, K))
+    _expect(w, "w", torch.bfloat16, (E, K, N), x)
+    _expect(dout, "dout", torch.bfloat16, (S, N), x)
+    _expect(silu_pre, "silu_pre", torch.bfloat16, (S, K), x)
+    _expect_experts(offsets, E, x)
+    _expect_status(status, x)
+    with _on(x.device, stream):
+        if grads is None:
+            grads = (torch.empty_like(x), torch.empty_like(w))
+        dx, dw = grads
+        _expect(dx, "dx", torch.bfloat16, (S, K), x)
+        _expect(dw, "dw", torch.bfloat16, (E, K, N), x)
+        st = lib().hstu_expert_proj_bwd(_ptr(dout), _ptr(x), _ptr(w), _ptr(offsets),
+                                        _ptr(silu_pre), S, E, K, N, _ptr(dx), _ptr(dw),
+                                        _ptr(status), _stream(None))
+    _check(st, "hstu_expert_proj_bwd")
+    return grads
+
+
+def expert_layer_fwd(x, residual, norm_weight, expert_ids, gates, w_in, w_out, *, ln_eps=1e-5,
+                     training=False, status=None, stream=None):
+    """A mixture-of-experts layer on tokens x [T, d_model] (bf16) behind a residual stream:
+    h = x + residual, each token's experts' SiLU(norm(h) w_in[e]) w_out[e], weighted by gates
+    [T, choices] and added to h.  w_in [E, d_model, d_ff], or (e4m3 [E, d_ff, d_model], scales
+    [E, d_ff]) for the 8-bit product (inference); w_out [E, d_ff, d_model].  Returns dict(o, sum,
+    rstd, routing, xs, pre, z, y); expert_layer_bwd takes it after training=True."""
+    eight = isinstance(w_in, (tuple, list))
+    if eight and training:
+        raise ValueError("the 8-bit product has no backward")
+    E = w_out.shape[0]
+    n = rms_norm_rows(x, norm_weight, residual, eps=ln_eps, e4m3=eight, training=training,
+                      stream=stream)
+    r = expert_sort(expert_ids, E, status=status, stream=stream)
+    pre = None
+    if eight:
+        xs, sc = expert_dispatch(n.y, r.slots, scales=n.scales, stream=stream)
+        z = expert_proj_e4m3(xs, sc, w_in[0], w_in[1], r.offsets, silu=True, status=status,
+                             stream=stream)
+    else:
+        xs = expert_dispatch(n.y, r.slots, stream=stream)
+        if training:
+            with _on(x.device, stream):
+                pre = torch.empty((xs.shape[0], w_in.shape[2]), dtype=x.dtype, device=x.device)
+        z = expert_proj(xs, w_in, r.offsets, silu=True, pre=pre, status=status, stream=stream)
+    y = expert_proj(z, w_out, r.offsets, status=status, stream=stream)
+    o = expert_combine(y, r.slots, gates, residual=n.sum, stream=stream)
+    return dict(o=o, sum=n.sum, rstd=n.rstd, routing=r, xs=xs, pre=pre, z=z, y=y)
+
+
+def expert_layer_bwd(do, saved, norm_weight, gates, w_in, w_out, *, status=None, stream=None):
+    """Gradients of expert_layer_fwd(..., training=True), whose result is `saved`: dict(dx (of x
+    and of residual alike), dnorm_weight, dgates, dw_in, dw_out)."""
+    r = saved["routing"]
+    dy, dgates = expert_combine_bwd(do, saved["y"], r.slots, gates, stream=stream)
+    dpre, dw_out = expert_proj_bwd(dy, saved["z"], w_out, r.offsets, silu_pre=saved["pre"],
+                                   status=status, stream=stream)
+    dxs, dw_in = expert_proj_bwd(dpre, saved["xs"], w_in, r.offsets, status=status, stream=stream)
+    dn = expert_dispatch_bwd(dxs, r.slots, stream=stream)
+    dx, dnw = rms_norm_rows_bwd(dn, saved["sum"], saved["rstd"], norm_weight, dsum=do,
+                                stream=stream)
+    return dict(dx=dx, dnorm_weight=dnw, dgates=dgates, dw_in=dw_in, dw_out=dw_out)
 
 
 def version() -> int:
