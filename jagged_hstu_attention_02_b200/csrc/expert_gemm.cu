@@ -16,6 +16,7 @@
 // Every wait is bounded.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "experts.h"
@@ -31,8 +32,10 @@ namespace {
 
 enum Product { P_FWD = 0, P_E4M3 = 1, P_DX = 2, P_DW = 3 };
 
-constexpr int EBM = 128;             // rows of an output tile (TMEM lanes)
+constexpr int EBM = 128;             // rows of a CTA's output tile (TMEM lanes)
+constexpr int EBN = 128;             // columns of the second operand that a CTA stages
 constexpr int kSlice = 128;          // bytes of the contraction per stage and row
+constexpr int kStages = 5;
 constexpr int kSmallBox = 16;        // rows of the small A box, for tiles with few rows
 constexpr int kEpiWarps = 8;
 constexpr int kEThreads = 32 * (2 + kEpiWarps);
@@ -53,37 +56,177 @@ struct EGemmArgs {
     int stall_test;                  // test only: the MMA warp first waits for nothing
 };
 
-template <int BN>
+// Shared memory of a CTA.  CG CTAs work on one tile of CG * 128 rows x CG * 128 columns: each
+// stages 128 rows of A and 128 columns of B, 32 KB per stage.
 struct ELayout {
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
     static constexpr int AB = EBM * kSlice;           // 16 KB
-    static constexpr int BB = BN * kSlice;
+    static constexpr int BB = EBN * kSlice;           // 16 KB
     static constexpr int A_OFF = 0;
-    static constexpr int B_OFF = STAGES * AB;
-    static constexpr int BAR_OFF = B_OFF + STAGES * BB;
-    static constexpr int TAB_OFF = BAR_OFF + 256;     // tile prefix and row starts
+    static constexpr int B_OFF = kStages * AB;
+    static constexpr int C_OFF = B_OFF + kStages * BB;      // 4 KB per epilogue warp
+    static constexpr int BAR_OFF = C_OFF + kEpiWarps * 4096;
+    static constexpr int TAB_OFF = BAR_OFF + 512;     // tile prefix and row starts
 };
 
-__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0,
+// TMA loads into this CTA's shared memory.  CG = 2: `bar` is an address in the pair's shared
+// memory, of this CTA's barrier or of the leader's.
+template <int CG>
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int c0,
                                         int c1)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
-        : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
 }
 
-// D (TMEM) += A (smem) B (smem), e4m3 values, fp32 accumulator: 32 of the contraction per MMA.
-__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate)
+template <int CG>
+__device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int c0,
+                                        int c1, int c2)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+}
+
+// Address of the leader's (rank 0) copy of `bar` in the pair's shared memory.
+__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+    return r;
+}
+
+// D (TMEM) += A (smem) B (smem), fp32 accumulator: 16 bf16 or 32 e4m3 of the contraction per
+// MMA.  CG = 2: both CTAs of the pair hold half of A's rows, B's columns and D's rows, at the
+// same shared-memory and TMEM addresses; one thread of the pair issues.
+#define HSTU_MMA(GROUP, KIND)                                              \
+    asm volatile(                                                          \
+        "{\n\t.reg .pred p;\n\t"                                           \
+        "setp.ne.b32 p, %4, 0;\n\t"                                        \
+        "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), \
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)              \
+        : "memory")
+
+template <int CG, bool E4M3>
+__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                     uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (CG == 1 && !E4M3) HSTU_MMA("1", "f16");
+    if constexpr (CG == 1 && E4M3) HSTU_MMA("1", "f8f6f4");
+    if constexpr (CG == 2 && !E4M3) HSTU_MMA("2", "f16");
+    if constexpr (CG == 2 && E4M3) HSTU_MMA("2", "f8f6f4");
+}
+#undef HSTU_MMA
+
+// Arrives on `bar` (CG = 2: of both CTAs) when the MMAs issued so far by this thread complete.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    if constexpr (CG == 1) {
+        umma_commit(bar);
+    } else {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+            ".b64 [%0], %1;" ::"r"(smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    }
+}
+
+// The same, on this CTA's barrier alone.
+template <int CG>
+__device__ __forceinline__ void commit_here(uint64_t *bar)
+{
+    if constexpr (CG == 1)
+        umma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_u32(bar))
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_take(uint32_t *slot, uint32_t ncols)
+{
+    if constexpr (CG == 1) {
+        tmem_alloc(slot, ncols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(slot)),
+                     "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_give(uint32_t taddr, uint32_t ncols)
+{
+    if constexpr (CG == 1)
+        tmem_dealloc(taddr, ncols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr),
+                     "r"(ncols)
+                     : "memory");
+}
+
+// All threads of both CTAs of a pair.
+__device__ __forceinline__ void pair_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One arrival on the leader's copy of `bar`, after what this thread did before.
+__device__ __forceinline__ void arrive_leader(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     leader_addr(bar))
+                 : "memory");
+}
+
+// mbar_wait for barriers on which the pair's other CTA arrives.
+__device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, long long limit)
+{
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
+            : "memory");
+        if (ok) return true;
+        if (clock64() - t0 > limit) return false;
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ bool warp_wait_cg(uint64_t *bar, uint32_t parity, long long limit)
+{
+    if constexpr (CG == 1) return warp_wait(bar, parity, limit);
+    return __all_sync(0xffffffffu, pair_wait(bar, parity, limit));
 }
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 A and B (format 0), K-major, fp32 D.
@@ -104,8 +247,10 @@ struct ExpertTable {
 };
 
 // Fills the table (all threads of the block).  An expert whose offsets are invalid has no rows.
+template <int CG>
 __device__ __forceinline__ void fill_table(const EGemmArgs &a, const ExpertTable &t, int32_t *wsum)
 {
+    constexpr int kRows = CG * EBM;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kEThreads / 32;
     int base = 0;
@@ -120,7 +265,7 @@ __device__ __forceinline__ void fill_table(const EGemmArgs &a, const ExpertTable
             }
             t.row0[e] = (int)lo;
             t.cnt[e] = (int)(hi - lo);
-            tiles = (int)((hi - lo + EBM - 1) / EBM);
+            tiles = (int)((hi - lo + kRows - 1) / kRows);
         }
         int s = tiles;
 #pragma unroll
@@ -143,32 +288,43 @@ __device__ __forceinline__ void fill_table(const EGemmArgs &a, const ExpertTable
     if (tid == 0) t.tile0[a.experts] = base;
 }
 
+// Bytes that a CTA with `rows` rows of A loads per stage.
+template <int P>
+__device__ __forceinline__ uint32_t stage_bytes(int rows)
+{
+    const bool small = P != P_DW && rows <= 64;
+    return ELayout::BB + (small ? (rows + kSmallBox - 1) / kSmallBox * kSmallBox * kSlice
+                                : (uint32_t)ELayout::AB);
+}
+
 struct ETile {
-    int e;         // expert
-    int m0, rows;  // first row (of the sorted rows; P_DW: of the matrix) and rows to store
-    int n0;        // first output column
+    int e;            // expert
+    int m0, rows;     // first row (of the sorted rows; P_DW: of the matrix) and rows to store
+    int n0;           // first output column
     int kbeg, kcnt;   // contraction: first index and length
 };
 
-template <int P, int BN>
+template <int P, int CG>
 __device__ __forceinline__ int tile_count(const EGemmArgs &a, const ExpertTable &t)
 {
-    const int nt = (a.n + BN - 1) / BN;
-    return P == P_DW ? a.experts * ((a.m + EBM - 1) / EBM) * nt : t.tile0[a.experts] * nt;
+    const int nt = (a.n + CG * EBN - 1) / (CG * EBN);
+    return P == P_DW ? a.experts * ((a.m + CG * EBM - 1) / (CG * EBM)) * nt
+                     : t.tile0[a.experts] * nt;
 }
 
-template <int P, int BN>
+template <int P, int CG>
 __device__ __forceinline__ ETile tile_of(const EGemmArgs &a, const ExpertTable &t, int tile)
 {
-    const int nt = (a.n + BN - 1) / BN;
+    constexpr int kRows = CG * EBM;
+    const int nt = (a.n + CG * EBN - 1) / (CG * EBN);
     ETile r;
-    r.n0 = (tile % nt) * BN;
+    r.n0 = (tile % nt) * (CG * EBN);
     const int q = tile / nt;
     if constexpr (P == P_DW) {
-        const int mt = (a.m + EBM - 1) / EBM;
+        const int mt = (a.m + kRows - 1) / kRows;
         r.e = q / mt;
-        r.m0 = (q % mt) * EBM;
-        r.rows = min(EBM, a.m - r.m0);
+        r.m0 = (q % mt) * kRows;
+        r.rows = min(kRows, a.m - r.m0);
         r.kbeg = t.row0[r.e];
         r.kcnt = t.cnt[r.e];
     } else {
@@ -178,47 +334,144 @@ __device__ __forceinline__ ETile tile_of(const EGemmArgs &a, const ExpertTable &
             if (t.tile0[mid] <= q) lo = mid; else hi = mid;
         }
         r.e = lo;
-        const int off = (q - t.tile0[lo]) * EBM;
+        const int off = (q - t.tile0[lo]) * kRows;
         r.m0 = t.row0[lo] + off;
-        r.rows = min(EBM, t.cnt[lo] - off);
+        r.rows = min(kRows, t.cnt[lo] - off);
         r.kbeg = 0;
         r.kcnt = a.kc;
     }
     return r;
 }
 
-enum EBar { E_FULL = 0, E_EMPTY = 8, EACC_FULL = 16, EACC_EMPTY = 18, E_DONE = 20, E_STALL = 21,
-            E_NBARS = 22 };
+// x * sigmoid(x) and its slope, on the hardware's exponential and reciprocal (2 ulp each).
+__device__ __forceinline__ float sigmoid_fast(float x)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
-template <int P, int BN>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// 16-byte piece c of row `row` of a warp's 32 x 128 bytes, swizzled so that 8 rows' pieces c,
+// and 8 pieces of a row, lie in different banks.
+__device__ __forceinline__ uint4 *staged(uint8_t *stage, int row, int c)
+{
+    return reinterpret_cast<uint4 *>(stage + row * 128 + ((c ^ (row & 7)) * 16));
+}
+
+// This lane's row (64 bf16) of the warp's 32 to shared memory, and from there whole rows to
+// out[(out0 + row) * n + nb ...], rows and columns that exist.
+__device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&o)[8], __nv_bfloat16 *out,
+                                           int64_t out0, int rows, int nb, int n)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *staged(stage, lane, i) = o[i];
+    __syncwarp();
+    const int r0 = lane / 8, col = nb + 8 * (lane & 7);
+    __nv_bfloat16 *at = out + (out0 + r0) * n + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 x = *staged(stage, 4 * i + r0, lane & 7);
+        if (4 * i + r0 < rows && col < n) *reinterpret_cast<uint4 *>(at) = x;
+        at += (int64_t)4 * n;
+    }
+    __syncwarp();
+}
+
+// 32 accumulator columns from nb on to bf16: scales, SiLU or the SiLU's slope applied in fp32
+// before the one rounding.  po: the product itself (P_FWD with pre); pv: this row's silu_pre.
+template <int P>
+__device__ __forceinline__ void convert32(const EGemmArgs &a, int e, int nb, bool none, float xs,
+                                          const uint32_t (&v)[32], const uint4 *pv, uint4 *o,
+                                          uint4 *po)
+{
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        float f[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : __uint_as_float(v[8 * h + x]);
+        if constexpr (P == P_E4M3) {
+            const int nc = nb + 8 * h;                   // n is a multiple of 8
+            if (nc < a.n) {
+                const float4 *sp = reinterpret_cast<const float4 *>(a.w_scales + (int64_t)e * a.n + nc);
+                const float4 s0 = __ldg(sp), s1 = __ldg(sp + 1);
+                f[0] *= xs * s0.x; f[1] *= xs * s0.y; f[2] *= xs * s0.z; f[3] *= xs * s0.w;
+                f[4] *= xs * s1.x; f[5] *= xs * s1.y; f[6] *= xs * s1.z; f[7] *= xs * s1.w;
+            }
+        }
+        if constexpr (P == P_DX) {
+            if (a.silu_pre) {
+                const uint32_t u4[4] = {pv[h].x, pv[h].y, pv[h].z, pv[h].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float p0 = __uint_as_float(u4[y] << 16);
+                    const float p1 = __uint_as_float(u4[y] & 0xFFFF0000u);
+                    const float s0 = sigmoid_fast(p0), s1 = sigmoid_fast(p1);
+                    f[2 * y] *= s0 * fmaf(p0, 1.f - s0, 1.f);
+                    f[2 * y + 1] *= s1 * fmaf(p1, 1.f - s1, 1.f);
+                }
+            }
+        }
+        if constexpr (P == P_FWD) {
+            if (a.pre) po[h] = pack8(f);
+        }
+        if constexpr (P == P_FWD || P == P_E4M3) {
+            if (a.silu) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) f[x] *= sigmoid_fast(f[x]);
+            }
+        }
+        o[h] = pack8(f);
+    }
+}
+
+// FULL (the leader's): both CTAs' copies of a stage have landed.  EMPTY (each CTA's): the MMAs
+// that read a stage are done.  P_DW with pairs, for a stage that needs zeroed rows: TAIL, the
+// other CTA's copies have landed (on its own barrier), READY, it has zeroed its rows.
+// (Both per stage: several tiles' last slices can be under way at once.)
+enum EBar { E_FULL = 0, E_EMPTY = 8, E_TAIL = 16, E_READY = 24, EACC_FULL = 32, EACC_EMPTY = 34,
+            E_DONE = 36, E_STALL = 37, E_NBARS = 38 };
+
+template <int P, int CG>
 __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_constant__ EGemmArgs a)
 {
-    using L = ELayout<BN>;
-    constexpr int ST = L::STAGES;
+    using L = ELayout;
+    constexpr int ST = kStages;
+    constexpr int BN = CG * EBN;                        // columns of the pair's tile
     constexpr int KB = P == P_E4M3 ? 128 : 64;          // contraction per stage
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR_OFF);
-    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::BAR_OFF + 8 * 24);
-    int32_t *wsum = reinterpret_cast<int32_t *>(sm + L::BAR_OFF + 8 * 25);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::BAR_OFF + 8 * 40);
+    int32_t *wsum = reinterpret_cast<int32_t *>(sm + L::BAR_OFF + 8 * 41);
     ExpertTable tab;
     tab.tile0 = reinterpret_cast<int32_t *>(sm + L::TAB_OFF);
     tab.row0 = tab.tile0 + a.experts + 1;
     tab.cnt = tab.row0 + a.experts;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
+    const int first = blockIdx.x / CG, stride = gridDim.x / CG;
     if (threadIdx.x == 0) {
         for (int x = 0; x < E_NBARS; ++x)
-            mbar_init(&bars[x], x == EACC_EMPTY || x == EACC_EMPTY + 1 ? kEpiWarps : 1);
+            mbar_init(&bars[x], x == EACC_EMPTY || x == EACC_EMPTY + 1 ? CG * kEpiWarps : 1);
         fence_mbar_init();
     }
-    if (warp == 2) tmem_alloc(slot, 2 * BN);
-    fill_table(a, tab, wsum);
+    if (warp == 2) tmem_take<CG>(slot, 2 * BN);
+    fill_table<CG>(a, tab, wsum);
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2) pair_sync();
     tc_fence_after();
     const uint32_t tmem = *slot;
     const uint32_t sm_base = smem_u32(sm);
-    const int ntiles = tile_count<P, BN>(a, tab);
+    const int ntiles = tile_count<P, CG>(a, tab);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -227,64 +480,81 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             prefetch_tmap(&a.tb);
             int g = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x) {
-                const ETile r = tile_of<P, BN>(a, tab, tile);
+            for (int tile = first; ok && tile < ntiles; tile += stride) {
+                const ETile r = tile_of<P, CG>(a, tab, tile);
                 const int kch = (r.kcnt + KB - 1) / KB;
-                const bool small = P != P_DW && r.rows <= 64;
-                const int boxes = small ? (r.rows + kSmallBox - 1) / kSmallBox : 1;
-                const uint32_t abytes = small ? boxes * kSmallBox * kSlice : L::AB;
+                const int m0 = r.m0 + rank * EBM, n0 = r.n0 + rank * EBN;
+                const int rows = max(0, min(EBM, r.rows - rank * EBM));   // of this CTA
+                const bool small = P != P_DW && rows <= 64;
+                const int boxes = (rows + kSmallBox - 1) / kSmallBox;
+                const uint32_t bytes = stage_bytes<P>(rows);
+                const uint32_t both = CG == 1 ? bytes : bytes + stage_bytes<P>(
+                    max(0, min(EBM, r.rows - EBM)));
                 for (int kc = 0; kc < kch; ++kc, ++g) {
                     const int s = g % ST;
                     if (g >= ST && !mbar_wait(&bars[E_EMPTY + s], ((g / ST) - 1) & 1, a.wait_limit)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&bars[E_FULL + s], abytes + L::BB);
                     uint8_t *as = sm + L::A_OFF + s * L::AB, *bs = sm + L::B_OFF + s * L::BB;
-                    uint64_t *full = &bars[E_FULL + s];
+                    const bool tail = CG == 2 && P == P_DW && r.kcnt - kc * KB < KB;
+                    if (rank == 0) mbar_arrive_expect_tx(&bars[E_FULL + s], tail ? bytes : both);
+                    else if (tail) mbar_arrive_expect_tx(&bars[E_TAIL + s], bytes);
+                    uint32_t full = smem_u32(&bars[E_FULL + s]);
+                    if (rank != 0) full = tail ? smem_u32(&bars[E_TAIL + s]) : leader_addr(&bars[E_FULL + s]);
                     if constexpr (P == P_DW) {
                         // both operands lie along their rows: blocks of 64 columns x 64 rows
                         for (int b = 0; b < EBM / 64; ++b)
-                            load_2d(as + b * 8192, &a.ta, full, r.m0 + 64 * b, r.kbeg + kc * KB);
-                        for (int b = 0; b < BN / 64; ++b)
-                            load_2d(bs + b * 8192, &a.tb, full, r.n0 + 64 * b, r.kbeg + kc * KB);
+                            load_2d<CG>(as + b * 8192, &a.ta, full, m0 + 64 * b, r.kbeg + kc * KB);
+                        for (int b = 0; b < EBN / 64; ++b)
+                            load_2d<CG>(bs + b * 8192, &a.tb, full, n0 + 64 * b, r.kbeg + kc * KB);
                     } else {
                         if (small) {
                             for (int b = 0; b < boxes; ++b)
-                                load_2d(as + b * kSmallBox * kSlice, &a.ta_small, full, kc * KB,
-                                        r.m0 + b * kSmallBox);
+                                load_2d<CG>(as + b * kSmallBox * kSlice, &a.ta_small, full, kc * KB,
+                                            m0 + b * kSmallBox);
                         } else {
-                            load_2d(as, &a.ta, full, kc * KB, r.m0);
+                            load_2d<CG>(as, &a.ta, full, kc * KB, m0);
                         }
                         if constexpr (P == P_FWD) {
-                            for (int b = 0; b < BN / 64; ++b)
-                                tma_load_3d(bs + b * 8192, &a.tb, full, r.n0 + 64 * b, kc * KB, r.e);
+                            for (int b = 0; b < EBN / 64; ++b)
+                                load_3d<CG>(bs + b * 8192, &a.tb, full, n0 + 64 * b, kc * KB, r.e);
                         } else {
-                            tma_load_3d(bs, &a.tb, full, kc * KB, r.n0, r.e);
+                            load_3d<CG>(bs, &a.tb, full, kc * KB, n0, r.e);
                         }
                     }
                 }
             }
             if (!ok) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
-            // every copy issued has landed before the block may exit
+            // Every copy issued has landed before the block may exit: seen on the barriers that
+            // it arrived on, or, by the other CTA of a pair, from the MMAs that have read it.
+            // (A producer that gave up has waited the limit since its last copy.)
             bool drained = true;
-            for (int x = g - 1; x >= 0 && x >= g - ST; --x)
-                drained &= mbar_wait(&bars[E_FULL + x % ST], (x / ST) & 1, kWaitLimitCycles);
+            if (rank == 0) {
+                for (int x = g - 1; x >= 0 && x >= g - ST; --x)
+                    drained &= mbar_wait(&bars[E_FULL + x % ST], (x / ST) & 1, kWaitLimitCycles);
+            } else {
+                for (int x = g > ST ? g - ST : 0; ok && drained && x < g; ++x)
+                    drained = mbar_wait(&bars[E_EMPTY + x % ST], (x / ST) & 1, kWaitLimitCycles);
+            }
             if (!drained) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
         }
     } else if (warp == 1) {
         // -------------------------------------------------------------------- MMA issuer
-        // the whole warp walks the tiles (it zeroes rows together); lane 0 issues
-        constexpr uint32_t idesc = P == P_E4M3 ? idesc_e4m3(EBM, BN)
-                                               : idesc_bf16(EBM, BN, P == P_DW, P != P_DX);
+        // the whole warp walks the tiles (it zeroes rows together); the leader's lane 0 issues,
+        // the other CTA's warp only zeroes its rows
+        constexpr uint32_t idesc = P == P_E4M3 ? idesc_e4m3(CG * EBM, BN)
+                                               : idesc_bf16(CG * EBM, BN, P == P_DW, P != P_DX);
         int g = 0, t = 0;
+        int tails = 0;                                  // bit s: parity of TAIL and READY[s]
         bool ok = !a.stall_test || warp_wait(&bars[E_STALL], 0, a.wait_limit);
-        for (int tile = blockIdx.x; ok && tile < ntiles; tile += gridDim.x) {
-            const ETile r = tile_of<P, BN>(a, tab, tile);
+        for (int tile = first; ok && tile < ntiles; tile += stride) {
+            const ETile r = tile_of<P, CG>(a, tab, tile);
             const int kch = (r.kcnt + KB - 1) / KB;
             if (kch == 0) continue;                     // (P_DW: an expert without rows)
             const int acc = t & 1;
-            if (t >= 2 && !warp_wait(&bars[EACC_EMPTY + acc], ((t >> 1) - 1) & 1, a.wait_limit)) {
+            if (rank == 0 && t >= 2 &&
+                !warp_wait_cg<CG>(&bars[EACC_EMPTY + acc], ((t >> 1) - 1) & 1, a.wait_limit)) {
                 ok = false;
                 break;
             }
@@ -293,24 +563,35 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             const uint32_t d = tmem + acc * BN;
             for (int kc = 0; kc < kch; ++kc, ++g) {
                 const int s = g % ST;
-                if (!warp_wait(&bars[E_FULL + s], (g / ST) & 1, a.wait_limit)) {
+                const int valid = r.kcnt - kc * KB;     // P_DW: rows of this slice
+                const bool tail = P == P_DW && valid < KB;
+                if (rank != 0 && !tail) continue;
+                if (!warp_wait(&bars[(rank == 0 ? E_FULL : E_TAIL) + s],
+                               (rank == 0 ? g / ST : tails >> s) & 1, a.wait_limit)) {
                     ok = false;
                     break;
                 }
-                if constexpr (P == P_DW) {
+                if (tail) {
                     // rows of this slice past the expert's end: zeros in both operands
-                    const int valid = r.kcnt - kc * KB;
-                    if (valid < KB) {
-                        const int per = (KB - valid) * 8;            // 16-byte pieces per block
-                        for (int b = 0; b < (EBM + BN) / 64; ++b) {
-                            uint8_t *blk = b < EBM / 64 ? sm + L::A_OFF + s * L::AB + b * 8192
-                                                        : sm + L::B_OFF + s * L::BB + (b - EBM / 64) * 8192;
-                            uint4 *z = reinterpret_cast<uint4 *>(blk + valid * 128);
-                            for (int x = lane; x < per; x += 32) z[x] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                    const int per = (KB - valid) * 8;                // 16-byte pieces per block
+                    for (int b = 0; b < (EBM + EBN) / 64; ++b) {
+                        uint8_t *blk = b < EBM / 64 ? sm + L::A_OFF + s * L::AB + b * 8192
+                                                    : sm + L::B_OFF + s * L::BB + (b - EBM / 64) * 8192;
+                        uint4 *z = reinterpret_cast<uint4 *>(blk + valid * 128);
+                        for (int x = lane; x < per; x += 32) z[x] = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if constexpr (CG == 2) {
+                        if (rank != 0) {
+                            if (lane == 0) arrive_leader(&bars[E_READY + s]);
+                        } else if (!warp_wait_cg<2>(&bars[E_READY + s], (tails >> s) & 1, a.wait_limit)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    tails ^= 1 << s;
+                    if (rank != 0) continue;
                 }
                 tc_fence_after();
                 if (lane == 0) {
@@ -326,40 +607,49 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                         const uint64_t bd = P == P_FWD || P == P_DW
                                                 ? sw128_desc(bb + kk * 2048, 8192, 1024)
                                                 : sw128_desc(bb + kk * 32, 16, 1024);
-                        if constexpr (P == P_E4M3)
-                            umma_f8_ss(d, ad, bd, idesc, (kc | kk) ? 1u : 0u);
-                        else
-                            umma_bf16_ss(d, ad, bd, idesc, (kc | kk) ? 1u : 0u);
+                        umma<CG, P == P_E4M3>(d, ad, bd, idesc, (kc | kk) ? 1u : 0u);
                     }
-                    umma_commit(&bars[E_EMPTY + s]);
+                    commit<CG>(&bars[E_EMPTY + s]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) umma_commit(&bars[EACC_FULL + acc]);
+            if (rank == 0 && lane == 0) commit<CG>(&bars[EACC_FULL + acc]);
             __syncwarp();
         }
         if (lane == 0) {
             if (!ok) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
-            umma_commit(&bars[E_DONE]);
-            if (!mbar_wait(&bars[E_DONE], 0, kWaitLimitCycles)) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
+            if (rank == 0) {
+                commit_here<CG>(&bars[E_DONE]);
+                if (!mbar_wait(&bars[E_DONE], 0, kWaitLimitCycles))
+                    egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
+            }
         }
         __syncwarp();
     } else {
         // -------------------------------------------------------------------- epilogue
-        // 64 columns per step: a lane converts its row's values into 8 chunks of 8 bf16, a
-        // transpose over groups of 8 lanes then lets 8 lanes store one row's 128 bytes
+        // 64 columns per step: a lane converts its row's values to bf16 and puts them, 16 bytes
+        // at a time and swizzled, into the warp's 4 KB of shared memory, from where 8 lanes
+        // store one row's 128 bytes side by side
         const int q = warp & 3;                          // TMEM lane quarter: rows 32q ..
         const int half = (warp - 2) >> 2;                // columns [half BN/2, (half+1) BN/2)
         const int rr = q * 32 + lane;                    // row of the tile == TMEM lane
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        const int j = lane & 7;                          // chunk this lane stores
+        uint8_t *stage = sm + L::C_OFF + (warp - 2) * 4096;
         int t = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-            const ETile r = tile_of<P, BN>(a, tab, tile);
+        for (int tile = first; tile < ntiles; tile += stride) {
+            const ETile r = tile_of<P, CG>(a, tab, tile);
+            const int m0 = r.m0 + rank * EBM;
+            // rows and columns of the tile that this warp stores (none: <= 0)
+            const int rows = min(EBM, r.rows - rank * EBM) - q * 32;
+            const int cbeg = half * (BN / 2);
+            const int cend = rows > 0 ? min((half + 1) * (BN / 2), a.n - r.n0) : cbeg;
             const bool none = P == P_DW && r.kcnt == 0;  // a gradient of zeros, without an MMA
             const int acc = t & 1;
+            const int64_t out0 = (P == P_DW ? (int64_t)r.e * a.m + m0 : (int64_t)m0) + q * 32;
+            float xs = 1.f;
+            if (P == P_E4M3 && lane < rows) xs = __ldg(a.x_scales + m0 + rr);
             if (!none) {
                 if (!warp_wait(&bars[EACC_FULL + acc], (t >> 1) & 1, a.wait_limit)) {
                     ok = false;
@@ -368,108 +658,67 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                 ++t;
                 tc_fence_after();
             }
-            const int64_t out0 = P == P_DW ? ((int64_t)r.e * a.m + r.m0) * a.n
-                                           : (int64_t)r.m0 * a.n;
-            const bool mine = rr < r.rows;
-            float xs = 1.f;
-            if (P == P_E4M3 && mine) xs = __ldg(a.x_scales + r.m0 + rr);
+            const uint32_t src = tmem + lane_base + acc * BN;
+            uint32_t v[32], w[32];
+            if (!none && cbeg < cend) {
+                __syncwarp();
+                tmem_ld32(src + cbeg, v);
+                tmem_ld32(src + cbeg + 32, w);
+            }
 #pragma unroll 1
-            for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 64) {
+            for (int c0 = cbeg; c0 < cend; c0 += 64) {
                 const int nb = r.n0 + c0;
-                if (nb >= a.n) break;                    // (warp-uniform)
-                if (q * 32 >= r.rows) break;             // no row of this warp is stored
-                __syncwarp();                            // the warp-wide TMEM loads below
-                uint32_t v[32], w[32];
+                uint4 pv[8];
+                if constexpr (P == P_DX) {
+                    if (a.silu_pre) {                    // whole rows in, each lane its own out
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int row = 4 * i + lane / 8, col = nb + 8 * (lane & 7);
+                            pv[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (row < rows && col < a.n)
+                                pv[i] = *reinterpret_cast<const uint4 *>(a.silu_pre + (out0 + row) * a.n + col);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) *staged(stage, 4 * i + lane / 8, lane & 7) = pv[i];
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) pv[i] = *staged(stage, lane, i);
+                        __syncwarp();
+                    }
+                }
                 if (!none) {
-                    tmem_ld32(tmem + lane_base + acc * BN + c0, v);
-                    tmem_ld32(tmem + lane_base + acc * BN + c0 + 32, w);
                     tmem_wait_ld();
                     reg_fence(v);
                     reg_fence(w);
                 }
-                float4 o[8], po[8];                      // 8 chunks of 8 bf16 (as 16 bytes)
-#pragma unroll
-                for (int hh = 0; hh < 8; ++hh) {
-                    float f[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        f[x] = none ? 0.f : __uint_as_float(hh < 4 ? v[8 * hh + x] : w[8 * hh - 32 + x]);
-                    const int nc = nb + 8 * hh;          // n is a multiple of 8
-                    if constexpr (P == P_E4M3) {
-                        if (nc < a.n) {
-                            const float4 *sp = reinterpret_cast<const float4 *>(
-                                a.w_scales + (int64_t)r.e * a.n + nc);
-                            const float4 s0 = __ldg(sp), s1 = __ldg(sp + 1);
-                            f[0] *= xs * s0.x; f[1] *= xs * s0.y; f[2] *= xs * s0.z; f[3] *= xs * s0.w;
-                            f[4] *= xs * s1.x; f[5] *= xs * s1.y; f[6] *= xs * s1.z; f[7] *= xs * s1.w;
-                        }
-                    }
-                    if constexpr (P == P_DX) {
-                        if (a.silu_pre && mine && nc < a.n) {
-                            const uint4 pv = *reinterpret_cast<const uint4 *>(
-                                a.silu_pre + (int64_t)(r.m0 + rr) * a.n + nc);
-                            const uint32_t u4[4] = {pv.x, pv.y, pv.z, pv.w};
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const float p0 = __uint_as_float(u4[y] << 16);
-                                const float p1 = __uint_as_float(u4[y] & 0xFFFF0000u);
-                                const float s0 = __fdividef(1.f, 1.f + __expf(-p0));
-                                const float s1 = __fdividef(1.f, 1.f + __expf(-p1));
-                                f[2 * y] *= s0 * (1.f + p0 * (1.f - s0));
-                                f[2 * y + 1] *= s1 * (1.f + p1 * (1.f - s1));
-                            }
-                        }
-                    }
-                    if constexpr (P == P_FWD) {
-                        if (a.pre)
-                            po[hh] = make_float4(__uint_as_float(pack_bf16x2(f[0], f[1])),
-                                                 __uint_as_float(pack_bf16x2(f[2], f[3])),
-                                                 __uint_as_float(pack_bf16x2(f[4], f[5])),
-                                                 __uint_as_float(pack_bf16x2(f[6], f[7])));
-                    }
-                    if constexpr (P == P_FWD || P == P_E4M3) {
-                        if (a.silu) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                f[x] = f[x] * __fdividef(1.0f, 1.0f + __expf(-f[x]));
-                        }
-                    }
-                    o[hh] = make_float4(__uint_as_float(pack_bf16x2(f[0], f[1])),
-                                        __uint_as_float(pack_bf16x2(f[2], f[3])),
-                                        __uint_as_float(pack_bf16x2(f[4], f[5])),
-                                        __uint_as_float(pack_bf16x2(f[6], f[7])));
-                }
-                // lane l now stores chunk j = l % 8 of rows l - j .. l - j + 7 of this warp
-                transpose_chunks<8>(o);
-                const int row = q * 32 + lane - j, col = nb + 8 * j;
-                const int64_t at = out0 + (int64_t)row * a.n + col;
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (row + c < r.rows && col < a.n)
-                        *reinterpret_cast<float4 *>(a.out + at + (int64_t)c * a.n) = o[c];
+                uint4 o[8], po[8];
+                const bool more = !none && c0 + 64 < cend;
+                convert32<P>(a, r.e, nb, none, xs, v, pv, o, po);
+                if (more) tmem_ld32(src + c0 + 64, v);
+                convert32<P>(a, r.e, nb + 32, none, xs, w, pv + 4, o + 4, po + 4);
+                if (more) tmem_ld32(src + c0 + 96, w);
+                store_rows(stage, o, a.out, out0, rows, nb, a.n);
                 if constexpr (P == P_FWD) {
-                    if (a.pre) {
-                        transpose_chunks<8>(po);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            if (row + c < r.rows && col < a.n)
-                                *reinterpret_cast<float4 *>(a.pre + at + (int64_t)c * a.n) = po[c];
-                    }
+                    if (a.pre) store_rows(stage, po, a.pre, out0, rows, nb, a.n);
                 }
             }
             if (!none) {
                 __syncwarp();
                 tc_fence_before();
-                warp_arrive(&bars[EACC_EMPTY + acc]);
+                if constexpr (CG == 1) warp_arrive(&bars[EACC_EMPTY + acc]);
+                else if (lane == 0) arrive_leader(&bars[EACC_EMPTY + acc]);
             }
         }
         if (!ok && lane == 0) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
     }
     tc_fence_before();
     __syncthreads();
+    // the leader's MMAs read both CTAs' shared memory and arrive on both CTAs' barriers
+    if constexpr (CG == 2) pair_sync();
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * BN);
+        tmem_give<CG>(tmem, 2 * BN);
     }
 }
 
@@ -506,50 +755,78 @@ bool encode(CUtensorMap *m, const void *base, bool bytes, int64_t d0, int64_t d1
            CUDA_SUCCESS;
 }
 
-template <int P, int BN>
-cudaError_t run_egemm(EGemmArgs &a, int64_t most_tiles, cudaStream_t st)
+// CTA pairs that the device runs at a time (cached per device ordinal).
+template <typename K>
+int most_pairs(K kern, int smem)
 {
-    using L = ELayout<BN>;
-    const int smem = L::TAB_OFF + (3 * a.experts + 1) * 4 + 1024;
-    static_assert(L::TAB_OFF + (3 * kMaxExperts + 1) * 4 + 1024 <= 232448, "shared memory");
-    auto k = expert_gemm_kernel<P, BN>;
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> cache[kMaxDev];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return num_sms() / 2;
+    int v = cache[dev].load(std::memory_order_relaxed);
+    if (v > 0) return v;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2));
+    cfg.blockDim = dim3(kEThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) {
+        cudaGetLastError();
+        v = num_sms() / 2;
+    }
+    cache[dev].store(v, std::memory_order_relaxed);
+    return v;
+}
+
+template <int P, int CG>
+cudaError_t run_egemm(const EGemmArgs &a, int64_t most_tiles, cudaStream_t st)
+{
+    const int smem = ELayout::TAB_OFF + (3 * a.experts + 1) * 4 + 1024;
+    static_assert(ELayout::TAB_OFF + (3 * kMaxExperts + 1) * 4 + 1024 <= 232448, "shared memory");
+    auto k = expert_gemm_kernel<P, CG>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = num_sms();
-    if (most_tiles < grid) grid = most_tiles;
-    if (grid <= 0) return cudaSuccess;
-    k<<<(unsigned)grid, kEThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    int64_t tiles = CG == 2 ? most_pairs(k, smem) : num_sms();
+    if (most_tiles < tiles) tiles = most_tiles;
+    if (tiles <= 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(CG * tiles));
+    cfg.blockDim = dim3(kEThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CG == 2 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 // The most row tiles that `rows` rows of `experts` experts can have.
-int64_t most_row_tiles(int64_t rows, int experts)
+int64_t most_row_tiles(int64_t rows, int experts, int tile)
 {
-    return rows / EBM + (rows < experts ? rows : experts);
+    return rows / tile + (rows < experts ? rows : experts);
 }
 
-// 256-wide tiles feed the tensor cores from shared memory at their full rate; 128-wide ones
-// are taken where the wider ones would leave the last wave of the persistent grid emptier.
-bool wide_tiles(int64_t row_tiles, int n)
-{
-    const int64_t sms = num_sms();
-    const int64_t wide = row_tiles * ((n + 255) / 256), narrow = row_tiles * ((n + 127) / 128);
-    const int64_t wide_time = 2 * ((wide + sms - 1) / sms), narrow_time = (narrow + sms - 1) / sms;
-    return wide_time <= narrow_time;
-}
-
+// Pairs of CTAs (256 x 256 tiles) read each operand half as often and reach the higher rate;
+// single CTAs (128 x 128) waste less on short experts and fill the device with fewer tiles.
 template <int P>
-cudaError_t run_by_width(EGemmArgs &a, const void *b, int64_t row_tiles, cudaStream_t st)
+cudaError_t run_by_size(const EGemmArgs &a, int64_t rows, cudaStream_t st)
 {
-    const bool wide = wide_tiles(row_tiles, a.n);
-    const int bn = wide ? 256 : 128;
-    bool ok = true;
-    if constexpr (P == P_FWD) ok = encode(&a.tb, b, false, a.n, a.kc, a.experts, 64);
-    if constexpr (P == P_E4M3) ok = encode(&a.tb, b, true, a.kc, a.n, a.experts, bn);
-    if constexpr (P == P_DX) ok = encode(&a.tb, b, false, a.kc, a.n, a.experts, bn);
-    if (!ok) return cudaErrorInvalidValue;
-    const int64_t tiles = row_tiles * ((a.n + bn - 1) / bn);
-    return wide ? run_egemm<P, 256>(a, tiles, st) : run_egemm<P, 128>(a, tiles, st);
+    auto tiles = [&](int cg) {
+        const int64_t bm = cg * EBM, bn = cg * EBN, nt = (a.n + bn - 1) / bn;
+        return (P == P_DW ? a.experts * ((a.m + bm - 1) / bm)
+                          : most_row_tiles(rows, a.experts, (int)bm)) * nt;
+    };
+    const bool pair = P == P_DW ? tiles(2) >= num_sms() / 2
+                                : rows >= (int64_t)a.experts * 192 && tiles(2) >= num_sms() / 2;
+    return pair ? run_egemm<P, 2>(a, tiles(2), st) : run_egemm<P, 1>(a, tiles(1), st);
 }
 
 EGemmArgs common(const ProjArgs &p)
@@ -572,7 +849,9 @@ cudaError_t launch_expert_proj(const ProjArgs &p, bool e4m3, cudaStream_t st)
     if (p.rows <= 0) return cudaSuccess;
     EGemmArgs a = common(p);
     if (!encode(&a.ta, p.x, e4m3, p.k, p.rows, 0, EBM) ||
-        !encode(&a.ta_small, p.x, e4m3, p.k, p.rows, 0, kSmallBox))
+        !encode(&a.ta_small, p.x, e4m3, p.k, p.rows, 0, kSmallBox) ||
+        !(e4m3 ? encode(&a.tb, p.w, true, p.k, p.n, p.experts, EBN)
+               : encode(&a.tb, p.w, false, p.n, p.k, p.experts, 64)))
         return cudaErrorInvalidValue;
     a.kc = p.k;
     a.n = p.n;
@@ -581,8 +860,7 @@ cudaError_t launch_expert_proj(const ProjArgs &p, bool e4m3, cudaStream_t st)
     a.w_scales = p.w_scales;
     a.out = reinterpret_cast<__nv_bfloat16 *>(p.out);
     a.pre = reinterpret_cast<__nv_bfloat16 *>(p.pre);
-    const int64_t rt = most_row_tiles(p.rows, p.experts);
-    return e4m3 ? run_by_width<P_E4M3>(a, p.w, rt, st) : run_by_width<P_FWD>(a, p.w, rt, st);
+    return e4m3 ? run_by_size<P_E4M3>(a, p.rows, st) : run_by_size<P_FWD>(a, p.rows, st);
 }
 
 cudaError_t launch_expert_proj_dx(const ProjArgs &p, cudaStream_t st)
@@ -590,13 +868,14 @@ cudaError_t launch_expert_proj_dx(const ProjArgs &p, cudaStream_t st)
     if (p.rows <= 0) return cudaSuccess;
     EGemmArgs a = common(p);
     if (!encode(&a.ta, p.dout, false, p.n, p.rows, 0, EBM) ||
-        !encode(&a.ta_small, p.dout, false, p.n, p.rows, 0, kSmallBox))
+        !encode(&a.ta_small, p.dout, false, p.n, p.rows, 0, kSmallBox) ||
+        !encode(&a.tb, p.w, false, p.n, p.k, p.experts, EBN))
         return cudaErrorInvalidValue;
     a.kc = p.n;
     a.n = p.k;
     a.silu_pre = reinterpret_cast<const __nv_bfloat16 *>(p.silu_pre);
     a.out = reinterpret_cast<__nv_bfloat16 *>(p.dx);
-    return run_by_width<P_DX>(a, p.w, most_row_tiles(p.rows, p.experts), st);
+    return run_by_size<P_DX>(a, p.rows, st);
 }
 
 cudaError_t launch_expert_proj_dw(const ProjArgs &p, cudaStream_t st)
@@ -610,10 +889,7 @@ cudaError_t launch_expert_proj_dw(const ProjArgs &p, cudaStream_t st)
     a.m = p.k;
     a.n = p.n;
     a.out = reinterpret_cast<__nv_bfloat16 *>(p.dw);
-    const int64_t rt = (int64_t)p.experts * ((p.k + EBM - 1) / EBM);
-    const bool wide = wide_tiles(rt, p.n);
-    const int64_t tiles = rt * ((p.n + (wide ? 255 : 127)) / (wide ? 256 : 128));
-    return wide ? run_egemm<P_DW, 256>(a, tiles, st) : run_egemm<P_DW, 128>(a, tiles, st);
+    return run_by_size<P_DW>(a, p.rows, st);
 }
 
 }  // namespace hstu

@@ -405,44 +405,63 @@ def layer_fwd(x, seq_offsets, num_contextuals, num_targets, timestamps, rel_bias
 
 F8 = torch.float8_e4m3fn
 _HERE = contextlib.nullcontext()
+# handle of a device's current stream, without the Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+# These calls run for a few microseconds on small batches, so what the host does around them is
+# kept short: addresses and the stream's handle go to the library as plain integers.
 
 
-def _on(device, stream):
-    """Where a call allocates and launches: the tensors' device, and `stream` (of that device)
+def _on(t, stream):
+    """Where a call on tensor t allocates and launches: t's device, and `stream` (of that device)
     or that device's current stream."""
-    if device.type != "cuda":
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
     if stream is not None:
-        if stream.device != device:
+        if stream.device_index != dev:
             raise ValueError("stream and tensors must be on the same device")
         return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         return _HERE
-    return torch.cuda.device(device)
+    return torch.cuda.device(dev)
+
+
+def _addr(t):
+    """Address of an optional tensor whose place _expect has checked."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 def _expect(t, name, dtype, shape, like=None):
     """Checks an optional tensor's type, shape and (like: a tensor) device."""
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if like is not None and t.device != like.device:
+    if like is not None and t.get_device() != like.get_device():
         raise ValueError("%s must be on %s" % (name, like.device))
 
 
 def _expect_slots(slots, like, name="slots"):
     if slots.dim() != 2:
         raise ValueError("%s must be [tokens, choices]" % name)
-    _expect(slots, name, torch.int32, slots.shape, like)
-    return slots.shape
+    shape = slots.shape
+    _expect(slots, name, torch.int32, shape, like)
+    return shape
 
 
 def _expect_status(status, like):
     if status is not None:
-        _expect(status.reshape(-1)[:1], "status", torch.int32, (1,), like)
+        if status.numel() < 1:
+            raise ValueError("status must hold an int32")
+        _expect(status, "status", torch.int32, status.shape, like)
 
 
 class RmsNorm(NamedTuple):
@@ -470,15 +489,12 @@ def rms_norm_rows(x, weight=None, residual=None, *, eps=1e-5, e4m3=False, group=
     _expect(weight, "weight", torch.float32, (width,), x)
     _expect(residual, "residual", x.dtype, x.shape, x)
     groups = -(-width // group) if group else 1
-    with _on(x.device, stream):
+    with _on(x, stream):
         if out is None:
-            dev = x.device
-            out = RmsNorm(torch.empty_like(x, dtype=F8 if e4m3 else x.dtype),
-                          torch.empty((rows, groups), dtype=torch.float32, device=dev)
-                          if e4m3 else None,
+            out = RmsNorm(torch.empty_like(x, dtype=F8) if e4m3 else torch.empty_like(x),
+                          x.new_empty((rows, groups), dtype=torch.float32) if e4m3 else None,
                           torch.empty_like(x) if residual is not None else x,
-                          torch.empty(rows, dtype=torch.float32, device=dev)
-                          if training else None)
+                          x.new_empty((rows,), dtype=torch.float32) if training else None)
         else:
             _expect(out.y, "out.y", F8 if e4m3 else x.dtype, x.shape, x)
             _expect(out.scales, "out.scales", torch.float32, (rows, groups), x)
@@ -489,12 +505,12 @@ def rms_norm_rows(x, weight=None, residual=None, *, eps=1e-5, e4m3=False, group=
         keep = out.sum if residual is not None else None
         if e4m3:
             st = lib().hstu_rms_norm_rows_e4m3(
-                _ptr(x), _ptr(residual), _ptr(weight), rows, width, eps, code, group, _ptr(out.y),
-                _ptr(out.scales), _ptr(keep), _ptr(out.rstd), _stream(None))
+                _addr(x), _addr(residual), _addr(weight), rows, width, eps, code, group, _addr(out.y),
+                _addr(out.scales), _addr(keep), _addr(out.rstd), _raw_stream(x.get_device()))
         else:
             st = lib().hstu_rms_norm_rows(
-                _ptr(x), _ptr(residual), _ptr(weight), rows, width, eps, code, _ptr(out.y),
-                _ptr(keep), _ptr(out.rstd), _stream(None))
+                _addr(x), _addr(residual), _addr(weight), rows, width, eps, code, _addr(out.y),
+                _addr(keep), _addr(out.rstd), _raw_stream(x.get_device()))
     _check(st, "hstu_rms_norm_rows")
     return out
 
@@ -511,7 +527,7 @@ def rms_norm_rows_bwd(dy, sum, rstd, weight=None, *, dsum=None, grads=None, work
     _expect(rstd, "rstd", torch.float32, (rows,), dy)
     _expect(weight, "weight", torch.float32, (width,), dy)
     _expect(dsum, "dsum", dy.dtype, dy.shape, dy)
-    with _on(dy.device, stream):
+    with _on(dy, stream):
         if grads is None:
             grads = (torch.empty_like(dy), None if weight is None else torch.empty_like(weight))
         dx, dw = grads
@@ -523,8 +539,8 @@ def rms_norm_rows_bwd(dy, sum, rstd, weight=None, *, dsum=None, grads=None, work
                    "hstu_rms_norm_rows_bwd_workspace_size")
             workspace = torch.empty(n.value, dtype=torch.uint8, device=dy.device)
         st = lib().hstu_rms_norm_rows_bwd(
-            _ptr(dy), _ptr(sum), _ptr(rstd), _ptr(weight), _ptr(dsum), rows, width, code, _ptr(dx),
-            _ptr(dw), _ptr(workspace), _bytes(workspace), _stream(None))
+            _addr(dy), _addr(sum), _addr(rstd), _addr(weight), _addr(dsum), rows, width, code, _addr(dx),
+            _addr(dw), _addr(workspace), _bytes(workspace), _raw_stream(dy.get_device()))
     _check(st, "hstu_rms_norm_rows_bwd")
     return grads
 
@@ -552,7 +568,7 @@ def expert_sort(expert_ids, num_experts: int, *, status=None, out: Optional[Rout
         raise ValueError("expert_ids must be int32 or int64")
     T, k = expert_ids.shape
     _expect_status(status, expert_ids)
-    with _on(expert_ids.device, stream):
+    with _on(expert_ids, stream):
         dev = expert_ids.device
         if out is None:
             out = Routing(torch.empty((T, k), dtype=torch.int32, device=dev),
@@ -569,9 +585,9 @@ def expert_sort(expert_ids, num_experts: int, *, status=None, out: Optional[Rout
             if n.value:
                 workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
         st = lib().hstu_expert_sort(
-            _ptr(expert_ids), 1 if expert_ids.dtype == torch.int64 else 0, T, k, num_experts,
-            _ptr(out.slots), _ptr(out.offsets), _ptr(out.rows), _ptr(status), _ptr(workspace),
-            _bytes(workspace), _stream(None))
+            _addr(expert_ids), 1 if expert_ids.dtype == torch.int64 else 0, T, k, num_experts,
+            _addr(out.slots), _addr(out.offsets), _addr(out.rows), _addr(status), _addr(workspace),
+            _bytes(workspace), _raw_stream(expert_ids.get_device()))
     _check(st, "hstu_expert_sort")
     return out
 
@@ -590,7 +606,7 @@ def expert_dispatch(x, slots, *, scales=None, out=None, scales_out=None, stream=
             raise ValueError("scales must be [tokens, n]")
         _expect(scales, "scales", torch.float32, (T, scales.shape[1]), x)
     row = x.shape[1:].numel()
-    with _on(x.device, stream):
+    with _on(x, stream):
         if out is None:
             out = torch.empty((T * k,) + tuple(x.shape[1:]), dtype=x.dtype, device=x.device)
         elif out.dim() < 1 or out.shape[1:] != x.shape[1:]:
@@ -603,9 +619,9 @@ def expert_dispatch(x, slots, *, scales=None, out=None, scales_out=None, stream=
             _expect(scales_out, "scales_out", torch.float32, (out.shape[0], scales.shape[1]), x)
         if row:
             st = lib().hstu_expert_dispatch(
-                _ptr(x), row * x.element_size(), _ptr(scales),
-                0 if scales is None else scales.shape[1], _ptr(slots), T, k, out.shape[0],
-                _ptr(out), _ptr(scales_out), _stream(None))
+                _addr(x), row * x.element_size(), _addr(scales),
+                0 if scales is None else scales.shape[1], _addr(slots), T, k, out.shape[0],
+                _addr(out), _addr(scales_out), _raw_stream(x.get_device()))
             _check(st, "hstu_expert_dispatch")
     return out if scales is None else (out, scales_out)
 
@@ -620,12 +636,12 @@ def expert_combine(y, slots, weights=None, *, residual=None, out=None, stream=No
     _expect(weights, "weights", torch.float32, (T, k), y)
     _expect(residual, "residual", y.dtype, shape, y)
     _expect(out, "out", y.dtype, shape, y)
-    with _on(y.device, stream):
+    with _on(y, stream):
         if out is None:
-            out = torch.empty(shape, dtype=y.dtype, device=y.device)
+            out = y.new_empty(shape)
         st = lib().hstu_expert_combine(
-            _ptr(y), _ptr(slots), _ptr(weights), _ptr(residual), T, k, y.shape[0], y.shape[1],
-            code, _ptr(out), _stream(None))
+            _addr(y), _addr(slots), _addr(weights), _addr(residual), T, k, y.shape[0], y.shape[1],
+            code, _addr(out), _raw_stream(y.get_device()))
     _check(st, "hstu_expert_combine")
     return out
 
@@ -639,15 +655,15 @@ def expert_combine_bwd(dout, y, slots, weights=None, *, grads=None, stream=None)
     code = dtype_code(y)
     _expect(dout, "dout", y.dtype, (T, y.shape[1]), y)
     _expect(weights, "weights", torch.float32, (T, k), y)
-    with _on(y.device, stream):
+    with _on(y, stream):
         if grads is None:
             grads = (torch.empty_like(y), None if weights is None else torch.empty_like(weights))
         dy, dw = grads
         _expect(dy, "dy", y.dtype, y.shape, y)
         _expect(dw, "dweights", torch.float32, (T, k), y)
         st = lib().hstu_expert_combine_bwd(
-            _ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, y.shape[0], y.shape[1], code,
-            _ptr(dy), _ptr(dw), _stream(None))
+            _addr(dout), _addr(y), _addr(slots), _addr(weights), T, k, y.shape[0], y.shape[1], code,
+            _addr(dy), _addr(dw), _raw_stream(y.get_device()))
     _check(st, "hstu_expert_combine_bwd")
     return grads
 
@@ -675,12 +691,12 @@ def expert_proj(x, w, offsets, *, silu=False, pre=None, out=None, status=None, s
     _expect(pre, "pre", torch.bfloat16, (S, N), x)
     _expect(out, "out", torch.bfloat16, (S, N), x)
     _expect_status(status, x)
-    with _on(x.device, stream):
+    with _on(x, stream):
         if out is None:
-            out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
-        st = lib().hstu_expert_proj(_ptr(x), _ptr(w), _ptr(offsets), S, E, K, N,
-                                    1 if silu else 0, _ptr(out), _ptr(pre), _ptr(status),
-                                    _stream(None))
+            out = x.new_empty((S, N))
+        st = lib().hstu_expert_proj(_addr(x), _addr(w), _addr(offsets), S, E, K, N,
+                                    1 if silu else 0, _addr(out), _addr(pre), _addr(status),
+                                    _raw_stream(x.get_device()))
     _check(st, "hstu_expert_proj")
     return out
 
@@ -701,12 +717,12 @@ def expert_proj_e4m3(x, x_scales, w, w_scales, offsets, *, silu=False, out=None,
     _expect_experts(offsets, E, x)
     _expect(out, "out", torch.bfloat16, (S, N), x)
     _expect_status(status, x)
-    with _on(x.device, stream):
+    with _on(x, stream):
         if out is None:
             out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
-        st = lib().hstu_expert_proj_e4m3(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales),
-                                         _ptr(offsets), S, E, K, N, 1 if silu else 0, _ptr(out),
-                                         _ptr(status), _stream(None))
+        st = lib().hstu_expert_proj_e4m3(_addr(x), _addr(x_scales), _addr(w), _addr(w_scales),
+                                         _addr(offsets), S, E, K, N, 1 if silu else 0, _addr(out),
+                                         _addr(status), _raw_stream(x.get_device()))
     _check(st, "hstu_expert_proj_e4m3")
     return out
 
@@ -725,15 +741,15 @@ def expert_proj_bwd(dout, x, w, offsets, *, silu_pre=None, grads=None, status=No
     _expect(silu_pre, "silu_pre", torch.bfloat16, (S, K), x)
     _expect_experts(offsets, E, x)
     _expect_status(status, x)
-    with _on(x.device, stream):
+    with _on(x, stream):
         if grads is None:
             grads = (torch.empty_like(x), torch.empty_like(w))
         dx, dw = grads
         _expect(dx, "dx", torch.bfloat16, (S, K), x)
         _expect(dw, "dw", torch.bfloat16, (E, K, N), x)
-        st = lib().hstu_expert_proj_bwd(_ptr(dout), _ptr(x), _ptr(w), _ptr(offsets),
-                                        _ptr(silu_pre), S, E, K, N, _ptr(dx), _ptr(dw),
-                                        _ptr(status), _stream(None))
+        st = lib().hstu_expert_proj_bwd(_addr(dout), _addr(x), _addr(w), _addr(offsets),
+                                        _addr(silu_pre), S, E, K, N, _addr(dx), _addr(dw),
+                                        _addr(status), _raw_stream(x.get_device()))
     _check(st, "hstu_expert_proj_bwd")
     return grads
 
@@ -760,7 +776,7 @@ def expert_layer_fwd(x, residual, norm_weight, expert_ids, gates, w_in, w_out, *
     else:
         xs = expert_dispatch(n.y, r.slots, stream=stream)
         if training:
-            with _on(x.device, stream):
+            with _on(x, stream):
                 pre = torch.empty((xs.shape[0], w_in.shape[2]), dtype=x.dtype, device=x.device)
         z = expert_proj(xs, w_in, r.offsets, silu=True, pre=pre, status=status, stream=stream)
     y = expert_proj(z, w_out, r.offsets, status=status, stream=stream)

@@ -444,6 +444,55 @@ def test_proj_bwd(counts, K, N):
         assert torch.equal(one[1], gw.t)
 
 
+@pytest.mark.parametrize("counts,K,N", [([399, 1], 72, 6400), ([130, 257, 600, 2, 63], 200, 3336),
+                                        ([1, 0, 63, 64, 65, 127, 129, 300, 2, 5000], 520, 1032)],
+                         ids=["wide", "ragged", "rows"])
+def test_products_large_enough_for_pairs_of_blocks(counts, K, N):
+    """Few and many rows per expert where the products run on pairs of blocks (256 x 256 tiles):
+    rows of no expert hold NaN, and short last slices of the weight gradients' contraction."""
+    x, w, off, S, E = _proj_case(counts, K, N, 3, K + N)
+    live = S - 3
+    do, pre = _rand(9, S, N), _rand(10, S, K)
+    do[live:] = float("nan")
+    out, p = Guarded((S, N), BF, 7.0), Guarded((S, N), BF, 7.0)
+    gx, gw = Guarded((S, K), BF, 7.0), Guarded((E, K, N), BF)
+    ops.expert_proj(x, w, off, silu=True, out=out.t, pre=p.t)
+    ops.expert_proj_bwd(do, x, w, off, silu_pre=pre, grads=(gx.t, gw.t))
+    for e, (a, b) in enumerate(zip(_np(off), _np(off)[1:])):
+        X, W, D = x[a:b].double(), w[e].double(), do[a:b].double()
+        q = pre[a:b].double()
+        slope = torch.sigmoid(q) * (1 + q * torch.sigmoid(-q))
+        r = X @ W
+        dot = _dot_tol(K, X.abs() @ W.abs())
+        for got, ref, tol in (
+                (p.t[a:b], r, r.abs() * 2 ** -8 + dot),
+                (out.t[a:b], r * torch.sigmoid(r), (r * torch.sigmoid(r)).abs() * (2 ** -8 + 2 ** -14)
+                 + 1.1 * dot),
+                (gx.t[a:b], (D @ W.T) * slope, ((D @ W.T) * slope).abs() * (2 ** -8 + 2 ** -14)
+                 + 1.1 * _dot_tol(N, D.abs() @ W.T.abs())),
+                (gw.t[e], X.T @ D, (X.T @ D).abs() * 2 ** -8 + _dot_tol(int(b - a), X.T.abs() @ D.abs()))):
+            assert ((got.double() - ref).abs() <= tol + 1e-30).all(), e
+    for g, rows in ((out, live), (p, live), (gx, live)):
+        assert (g.t[rows:] == 7).all()
+    for g in (out, p, gx, gw):
+        g.check("pairs")
+    if K % 16 == 0 or K == 200:
+        K8 = K // 16 * 16
+        xq = (x[:, :K8].float() * 50).nan_to_num().clamp(-448, 448).to(ops.F8).contiguous()
+        wq = (w.float().transpose(1, 2) * 200)[:, :, :K8].clamp(-448, 448).to(ops.F8).contiguous()
+        xs, ws = torch.rand(S, device="cuda") * 0.02, torch.rand(E, N, device="cuda") * 0.005
+        out = Guarded((S, N), BF, 7.0)
+        ops.expert_proj_e4m3(xq, xs, wq, ws, off, out=out.t)
+        for e, (a, b) in enumerate(zip(_np(off), _np(off)[1:])):
+            X = xq[a:b].double() * xs[a:b, None].double()
+            W = (wq[e].double() * ws[e][:, None].double()).T
+            r = X @ W
+            tol = r.abs() * (2 ** -8 + 3 * U) + _dot_tol(K8, X.abs() @ W.abs())
+            assert ((out.t[a:b].double() - r).abs() <= tol + 1e-30).all(), e
+        assert (out.t[live:] == 7).all()
+        out.check("pairs e4m3")
+
+
 def test_proj_without_rows():
     x, w, off, _, _ = _proj_case([0, 0], 64, 64, 0, 1)
     assert ops.expert_proj(x, w, off).shape == (0, 64)
