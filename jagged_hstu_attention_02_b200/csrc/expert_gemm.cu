@@ -37,7 +37,7 @@ constexpr int EBN = 128;             // columns of the second operand that a CTA
 constexpr int kSlice = 128;          // bytes of the contraction per stage and row
 constexpr int kStages = 5;
 constexpr int kSmallBox = 16;        // rows of the small A box, for tiles with few rows
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kEThreads = 32 * (2 + kEpiWarps);
 
 struct EGemmArgs {
@@ -63,8 +63,8 @@ struct ELayout {
     static constexpr int BB = EBN * kSlice;           // 16 KB
     static constexpr int A_OFF = 0;
     static constexpr int B_OFF = kStages * AB;
-    static constexpr int C_OFF = B_OFF + kStages * BB;      // 4 KB per epilogue warp
-    static constexpr int BAR_OFF = C_OFF + kEpiWarps * 4096;
+    static constexpr int C_OFF = B_OFF + kStages * BB;      // 2 KB per epilogue warp
+    static constexpr int BAR_OFF = C_OFF + kEpiWarps * 2048;
     static constexpr int TAB_OFF = BAR_OFF + 512;     // tile prefix and row starts
 };
 
@@ -200,6 +200,15 @@ __device__ __forceinline__ void pair_sync()
 __device__ __forceinline__ void arrive_leader(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     leader_addr(bar))
+                 : "memory");
+}
+
+// The same without ordering this thread's memory: for what it has read from TMEM into registers
+// (a release would also wait for its stores to global memory, which cost more than the MMAs).
+__device__ __forceinline__ void arrive_leader_relaxed(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                      leader_addr(bar))
                  : "memory");
 }
@@ -358,29 +367,29 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
                       pack_bf16x2(f[6], f[7]));
 }
 
-// 16-byte piece c of row `row` of a warp's 32 x 128 bytes, swizzled so that 8 rows' pieces c,
-// and 8 pieces of a row, lie in different banks.
+// 16-byte piece c of row `row` of a warp's 32 x 64 bytes, swizzled so that 8 rows' pieces c, and
+// the pieces of 2 rows, lie in different banks.
 __device__ __forceinline__ uint4 *staged(uint8_t *stage, int row, int c)
 {
-    return reinterpret_cast<uint4 *>(stage + row * 128 + ((c ^ (row & 7)) * 16));
+    return reinterpret_cast<uint4 *>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
 }
 
-// This lane's row (64 bf16) of the warp's 32 to shared memory, and from there whole rows to
+// This lane's row (32 bf16) of the warp's 32 to shared memory, and from there 4 lanes a row to
 // out[(out0 + row) * n + nb ...], rows and columns that exist.
-__device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&o)[8], __nv_bfloat16 *out,
+__device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&o)[4], __nv_bfloat16 *out,
                                            int64_t out0, int rows, int nb, int n)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *staged(stage, lane, i) = o[i];
+    for (int i = 0; i < 4; ++i) *staged(stage, lane, i) = o[i];
     __syncwarp();
-    const int r0 = lane / 8, col = nb + 8 * (lane & 7);
+    const int r0 = lane / 4, col = nb + 8 * (lane & 3);
     __nv_bfloat16 *at = out + (out0 + r0) * n + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint4 x = *staged(stage, 4 * i + r0, lane & 7);
-        if (4 * i + r0 < rows && col < n) *reinterpret_cast<uint4 *>(at) = x;
-        at += (int64_t)4 * n;
+    for (int i = 0; i < 4; ++i) {
+        const uint4 x = *staged(stage, 8 * i + r0, lane & 3);
+        if (8 * i + r0 < rows && col < n) *reinterpret_cast<uint4 *>(at) = x;
+        at += (int64_t)8 * n;
     }
     __syncwarp();
 }
@@ -389,8 +398,8 @@ __device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&o)[8], 
 // before the one rounding.  po: the product itself (P_FWD with pre); pv: this row's silu_pre.
 template <int P>
 __device__ __forceinline__ void convert32(const EGemmArgs &a, int e, int nb, bool none, float xs,
-                                          const uint32_t (&v)[32], const uint4 *pv, uint4 *o,
-                                          uint4 *po)
+                                          const uint32_t (&v)[32], const uint4 (&pv)[4],
+                                          uint4 (&o)[4], uint4 (&po)[4])
 {
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -628,14 +637,15 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
         __syncwarp();
     } else {
         // -------------------------------------------------------------------- epilogue
-        // 64 columns per step: a lane converts its row's values to bf16 and puts them, 16 bytes
-        // at a time and swizzled, into the warp's 4 KB of shared memory, from where 8 lanes
-        // store one row's 128 bytes side by side
+        // 32 columns per step: a lane converts its row's values to bf16 and puts them, 16 bytes
+        // at a time and swizzled, into the warp's 2 KB of shared memory, from where 4 lanes
+        // store one row's 64 bytes side by side.  A step is a chain of latencies (TMEM, shared
+        // memory, stores), so four warps per lane quarter work side by side.
         const int q = warp & 3;                          // TMEM lane quarter: rows 32q ..
-        const int half = (warp - 2) >> 2;                // columns [half BN/2, (half+1) BN/2)
+        const int quarter = (warp - 2) >> 2;             // a quarter of the columns
         const int rr = q * 32 + lane;                    // row of the tile == TMEM lane
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        uint8_t *stage = sm + L::C_OFF + (warp - 2) * 4096;
+        uint8_t *stage = sm + L::C_OFF + (warp - 2) * 2048;
         int t = 0;
         bool ok = true;
         for (int tile = first; tile < ntiles; tile += stride) {
@@ -643,8 +653,8 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             const int m0 = r.m0 + rank * EBM;
             // rows and columns of the tile that this warp stores (none: <= 0)
             const int rows = min(EBM, r.rows - rank * EBM) - q * 32;
-            const int cbeg = half * (BN / 2);
-            const int cend = rows > 0 ? min((half + 1) * (BN / 2), a.n - r.n0) : cbeg;
+            const int cbeg = quarter * (BN / 4);
+            const int cend = rows > 0 ? min((quarter + 1) * (BN / 4), a.n - r.n0) : cbeg;
             const bool none = P == P_DW && r.kcnt == 0;  // a gradient of zeros, without an MMA
             const int acc = t & 1;
             const int64_t out0 = (P == P_DW ? (int64_t)r.e * a.m + m0 : (int64_t)m0) + q * 32;
@@ -659,45 +669,38 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                 tc_fence_after();
             }
             const uint32_t src = tmem + lane_base + acc * BN;
-            uint32_t v[32], w[32];
-            if (!none && cbeg < cend) {
-                __syncwarp();
-                tmem_ld32(src + cbeg, v);
-                tmem_ld32(src + cbeg + 32, w);
-            }
 #pragma unroll 1
-            for (int c0 = cbeg; c0 < cend; c0 += 64) {
+            for (int c0 = cbeg; c0 < cend; c0 += 32) {
                 const int nb = r.n0 + c0;
-                uint4 pv[8];
+                uint32_t v[32];
+                if (!none) {
+                    __syncwarp();                        // the warp-wide TMEM load
+                    tmem_ld32(src + c0, v);
+                }
+                uint4 pv[4];
                 if constexpr (P == P_DX) {
-                    if (a.silu_pre) {                    // whole rows in, each lane its own out
+                    if (a.silu_pre) {                    // 4 lanes a row in, each lane its own out
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int row = 4 * i + lane / 8, col = nb + 8 * (lane & 7);
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 8 * i + lane / 4, col = nb + 8 * (lane & 3);
                             pv[i] = make_uint4(0u, 0u, 0u, 0u);
                             if (row < rows && col < a.n)
                                 pv[i] = *reinterpret_cast<const uint4 *>(a.silu_pre + (out0 + row) * a.n + col);
                         }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) *staged(stage, 8 * i + lane / 4, lane & 3) = pv[i];
                         __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) *staged(stage, 4 * i + lane / 8, lane & 7) = pv[i];
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) pv[i] = *staged(stage, lane, i);
+                        for (int i = 0; i < 4; ++i) pv[i] = *staged(stage, lane, i);
                         __syncwarp();
                     }
                 }
                 if (!none) {
                     tmem_wait_ld();
                     reg_fence(v);
-                    reg_fence(w);
                 }
-                uint4 o[8], po[8];
-                const bool more = !none && c0 + 64 < cend;
+                uint4 o[4], po[4];
                 convert32<P>(a, r.e, nb, none, xs, v, pv, o, po);
-                if (more) tmem_ld32(src + c0 + 64, v);
-                convert32<P>(a, r.e, nb + 32, none, xs, w, pv + 4, o + 4, po + 4);
-                if (more) tmem_ld32(src + c0 + 96, w);
                 store_rows(stage, o, a.out, out0, rows, nb, a.n);
                 if constexpr (P == P_FWD) {
                     if (a.pre) store_rows(stage, po, a.pre, out0, rows, nb, a.n);
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                 __syncwarp();
                 tc_fence_before();
                 if constexpr (CG == 1) warp_arrive(&bars[EACC_EMPTY + acc]);
-                else if (lane == 0) arrive_leader(&bars[EACC_EMPTY + acc]);
+                else if (lane == 0) arrive_leader_relaxed(&bars[EACC_EMPTY + acc]);
             }
         }
         if (!ok && lane == 0) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
