@@ -394,10 +394,11 @@ __device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&o)[4], 
     __syncwarp();
 }
 
-// 32 accumulator columns from nb on to bf16: scales, SiLU or the SiLU's slope applied in fp32
-// before the one rounding.  po: the product itself (P_FWD with pre); pv: this row's silu_pre.
+// 32 accumulator columns to bf16: scales, SiLU or the SiLU's slope applied in fp32 before the
+// one rounding.  xs, ws: the row's scale and the columns' (P_E4M3); pv: this row's silu_pre
+// (P_DX); po: the product itself (P_FWD with pre).
 template <int P>
-__device__ __forceinline__ void convert32(const EGemmArgs &a, int e, int nb, bool none, float xs,
+__device__ __forceinline__ void convert32(const EGemmArgs &a, bool none, float xs, const float4 *ws,
                                           const uint32_t (&v)[32], const uint4 (&pv)[4],
                                           uint4 (&o)[4], uint4 (&po)[4])
 {
@@ -407,13 +408,9 @@ __device__ __forceinline__ void convert32(const EGemmArgs &a, int e, int nb, boo
 #pragma unroll
         for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : __uint_as_float(v[8 * h + x]);
         if constexpr (P == P_E4M3) {
-            const int nc = nb + 8 * h;                   // n is a multiple of 8
-            if (nc < a.n) {
-                const float4 *sp = reinterpret_cast<const float4 *>(a.w_scales + (int64_t)e * a.n + nc);
-                const float4 s0 = __ldg(sp), s1 = __ldg(sp + 1);
-                f[0] *= xs * s0.x; f[1] *= xs * s0.y; f[2] *= xs * s0.z; f[3] *= xs * s0.w;
-                f[4] *= xs * s1.x; f[5] *= xs * s1.y; f[6] *= xs * s1.z; f[7] *= xs * s1.w;
-            }
+            const float4 s0 = ws[2 * h], s1 = ws[2 * h + 1];
+            f[0] *= xs * s0.x; f[1] *= xs * s0.y; f[2] *= xs * s0.z; f[3] *= xs * s0.w;
+            f[4] *= xs * s1.x; f[5] *= xs * s1.y; f[6] *= xs * s1.z; f[7] *= xs * s1.w;
         }
         if constexpr (P == P_DX) {
             if (a.silu_pre) {
@@ -658,8 +655,18 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             const bool none = P == P_DW && r.kcnt == 0;  // a gradient of zeros, without an MMA
             const int acc = t & 1;
             const int64_t out0 = (P == P_DW ? (int64_t)r.e * a.m + m0 : (int64_t)m0) + q * 32;
-            float xs = 1.f;
-            if (P == P_E4M3 && lane < rows) xs = __ldg(a.x_scales + m0 + rr);
+            // scales: this lane's row's, and per step this lane's column's, fetched while the
+            // accumulator is not there yet (loading them column by column in the step, through
+            // L1, took as long as the MMAs of 512 of the contraction)
+            float xs = 1.f, ws[BN / 128];
+            if constexpr (P == P_E4M3) {
+                if (lane < rows) xs = __ldg(a.x_scales + m0 + rr);
+#pragma unroll
+                for (int i = 0; i < BN / 128; ++i) {
+                    const int col = r.n0 + cbeg + 32 * i + lane;
+                    ws[i] = col < a.n ? __ldg(a.w_scales + (int64_t)r.e * a.n + col) : 0.f;
+                }
+            }
             if (!none) {
                 if (!warp_wait(&bars[EACC_FULL + acc], (t >> 1) & 1, a.wait_limit)) {
                     ok = false;
@@ -669,29 +676,31 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                 tc_fence_after();
             }
             const uint32_t src = tmem + lane_base + acc * BN;
-#pragma unroll 1
-            for (int c0 = cbeg; c0 < cend; c0 += 32) {
-                const int nb = r.n0 + c0;
+#pragma unroll
+            for (int i = 0; i < BN / 128; ++i) {
+                const int c0 = cbeg + 32 * i, nb = r.n0 + c0;
+                if (c0 >= cend) break;
                 uint32_t v[32];
                 if (!none) {
                     __syncwarp();                        // the warp-wide TMEM load
                     tmem_ld32(src + c0, v);
                 }
                 uint4 pv[4];
+                if constexpr (P == P_E4M3) reinterpret_cast<float *>(stage)[lane] = ws[i];
                 if constexpr (P == P_DX) {
                     if (a.silu_pre) {                    // 4 lanes a row in, each lane its own out
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = 8 * i + lane / 4, col = nb + 8 * (lane & 3);
-                            pv[i] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int u = 0; u < 4; ++u) {
+                            const int row = 8 * u + lane / 4, col = nb + 8 * (lane & 3);
+                            pv[u] = make_uint4(0u, 0u, 0u, 0u);
                             if (row < rows && col < a.n)
-                                pv[i] = *reinterpret_cast<const uint4 *>(a.silu_pre + (out0 + row) * a.n + col);
+                                pv[u] = *reinterpret_cast<const uint4 *>(a.silu_pre + (out0 + row) * a.n + col);
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) *staged(stage, 8 * i + lane / 4, lane & 3) = pv[i];
+                        for (int u = 0; u < 4; ++u) *staged(stage, 8 * u + lane / 4, lane & 3) = pv[u];
                         __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) pv[i] = *staged(stage, lane, i);
+                        for (int u = 0; u < 4; ++u) pv[u] = *staged(stage, lane, u);
                         __syncwarp();
                     }
                 }
@@ -700,7 +709,9 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                     reg_fence(v);
                 }
                 uint4 o[4], po[4];
-                convert32<P>(a, r.e, nb, none, xs, v, pv, o, po);
+                __syncwarp();
+                convert32<P>(a, none, xs, reinterpret_cast<const float4 *>(stage), v, pv, o, po);
+                __syncwarp();
                 store_rows(stage, o, a.out, out0, rows, nb, a.n);
                 if constexpr (P == P_FWD) {
                     if (a.pre) store_rows(stage, po, a.pre, out0, rows, nb, a.n);
