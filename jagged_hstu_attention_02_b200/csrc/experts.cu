@@ -279,10 +279,9 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     if (a.weights && lane < a.choices) weight = a.weights[t * a.choices + lane];
     const T *y = reinterpret_cast<const T *>(a.y);
     for (int i0 = (warp % wpr) * 256; i0 < a.width; i0 += 256 * wpr) {
-        const int i = i0 + lane * 8;
         float acc[8];
         if (a.resid) {
-            load8<VEC>(reinterpret_cast<const T *>(a.resid) + t * a.width, i, a.width, acc);
+            load8<VEC>(reinterpret_cast<const T *>(a.resid) + t * a.width, i0, a.width, acc);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = 0.f;
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(32 * kRowWarps)
             for (int u = 0; u < 4; ++u) {
                 // lanes from `choices` up hold -1
                 const int s = __shfl_sync(kFullMask, mine, j0 + u);
-                load8<VEC>(y + (s < 0 ? 0 : (int64_t)s * a.width), i, s < 0 ? 0 : a.width, f[u]);
+                load8<VEC>(y + (s < 0 ? 0 : (int64_t)s * a.width), i0, s < 0 ? 0 : a.width, f[u]);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(32 * kRowWarps)
                 }
             }
         }
-        store8<VEC>(reinterpret_cast<T *>(a.out) + t * a.width, i, a.width, acc);
+        store8<VEC>(reinterpret_cast<T *>(a.out) + t * a.width, i0, a.width, acc);
     }
 }
 
@@ -328,9 +327,8 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 #pragma unroll
     for (int j = 0; j < KM; ++j) dot[j] = 0.f;
     for (int i0 = (warp % wpr) * 256; i0 < width; i0 += 256 * wpr) {
-        const int i = i0 + lane * 8;
         float g[8];
-        load8<VEC>(reinterpret_cast<const T *>(a.dout) + t * a.width, i, width, g);
+        load8<VEC>(reinterpret_cast<const T *>(a.dout) + t * a.width, i0, width, g);
 #pragma unroll
         for (int j = 0; j < KM; ++j) {
             const int s = __shfl_sync(kFullMask, mine, j);
@@ -338,14 +336,14 @@ __global__ void __launch_bounds__(32 * kRowWarps)
             if (s < 0) continue;                       // (warp-uniform)
             if (a.dweights) {
                 float f[8];
-                load8<VEC>(y + (int64_t)s * a.width, i, width, f);
+                load8<VEC>(y + (int64_t)s * a.width, i0, width, f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dot[j] = fmaf(g[e], f[e], dot[j]);
             }
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = w * g[e];
-            store8<VEC>(dy + (int64_t)s * a.width, i, width, o);
+            store8<VEC>(dy + (int64_t)s * a.width, i0, width, o);
         }
     }
     if (!a.dweights) return;

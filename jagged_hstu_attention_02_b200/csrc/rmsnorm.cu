@@ -6,24 +6,47 @@
 //   backward at the stored h, with xh = h * rstd and g = dy * weight:
 //     dx = rstd * (g - xh * mean(g * xh)) + dsum;   dweight = sum over rows of dy * xh
 //
-// Bound by memory: every tensor is read or written once, so a row stays in registers between
-// the sum of squares and the output.  W warps share a row (each thread NC chunks of 8
-// elements), and a block of several narrow rows or one wide row keeps 256 threads or more.
+// Bound by memory: every tensor is read or written once.  W warps (a group) share a row, each
+// thread 2 chunks of 8 elements, kept in registers between the sum of squares and the output.
+// A group's chain per row (load, sum, scale, store) is all latency, so with more rows than
+// groups the groups stay and their rows arrive ahead of them through a ring of bulk copies in
+// shared memory (RING); with fewer, or where rows do not start on 16 bytes, they load directly.
 // The forward normalises the fp32 sum, before it is rounded to the stored h.
 #include <cuda_fp8.h>
+#include <math_constants.h>
 
-#include <type_traits>
+#include <algorithm>
 
 #include "experts.h"
 #include "kernels.h"
 #include "lnrow.cuh"
 #include "rowvec.cuh"
+#include "sm100.cuh"
 
 namespace hstu {
 
 namespace {
 
+using sm100::mbar_arrive_expect_tx;
+using sm100::mbar_init;
+using sm100::mbar_try_wait;
+using sm100::named_bar_sync;
+using sm100::smem_u32;
+
+constexpr int NC = 2;                   // chunks of 8 elements per thread
+constexpr int kMaxRing = 4;
 constexpr float kE4m3Max = 448.f;
+
+// How rows are read: through the ring, directly in 16-byte pieces, or element by element.
+enum Access { RING, DIRECT, ELEMENTS };
+
+template <int W> struct NormShape {
+    static constexpr int kGroups = W < 8 ? 8 / W : 1;      // per block
+    static constexpr int kThreads = 32 * W * kGroups;
+    // blocks that share an SM: the forward at 64 registers a thread, the backward at 128
+    static constexpr int kFwdBlocks = 1024 / kThreads;
+    static constexpr int kBwdBlocks = kThreads >= 512 ? 1 : 512 / kThreads;
+};
 
 // The largest magnitude that a group's scale maps to 448: its own, kept away from where
 // 448 / m overflows; 0 for a group of zeros, whose scale and values are then 0.
@@ -32,42 +55,94 @@ __device__ __forceinline__ float scale_top(float m)
     return m > 0.f ? fmaxf(m, 7.888609e-31f /* 2^-100 */) : 0.f;
 }
 
-// Sum over the W warps of each row group of the block; every thread gets its group's sum.
 template <int W>
-__device__ __forceinline__ float group_sum(float v, float *buf)
+__device__ __forceinline__ void group_sync()
 {
-    v = warp_sum(v);
-    if constexpr (W == 1) return v;
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) buf[warp] = v;
-    __syncthreads();
-    float s = 0.f;
-    const float *g = buf + warp / W * W;
-#pragma unroll
-    for (int i = 0; i < W; ++i) s += g[i];
-    return s;
+    if constexpr (W == 1) __syncwarp();
+    else if constexpr (W >= 8) __syncthreads();
+    else named_bar_sync(1 + threadIdx.x / (32 * W), 32 * W);
 }
 
-template <int W>
-__device__ __forceinline__ float group_max(float v, float *buf)
+// Sum (or maximum) over the W warps of the row group; every thread gets it.
+template <int W, bool MAX>
+__device__ __forceinline__ float group_reduce(float v, float *buf)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
-    if constexpr (W == 1) return v;
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) buf[warp] = v;
-    __syncthreads();
-    float s = 0.f;
-    const float *g = buf + warp / W * W;
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(kFullMask, v, o);
+        v = MAX ? fmaxf(v, u) : v + u;
+    }
+    if constexpr (W > 1) {
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) buf[warp] = v;
+        group_sync<W>();
+        const float *g = buf + warp / W * W;
+        v = g[0];
 #pragma unroll
-    for (int i = 0; i < W; ++i) s = fmaxf(s, g[i]);
-    return s;
+        for (int i = 1; i < W; ++i) v = MAX ? fmaxf(v, g[i]) : v + g[i];
+    }
+    return v;
+}
+
+// A group's ring of `depth` stages, each one row of every input; `full` its barriers.
+struct Ring {
+    uint8_t *base;
+    uint64_t *full;
+    int depth, stage_bytes;
+};
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void ring_fill(const Ring &r, int stage, const uint8_t *const (&in)[N],
+                                          int64_t row, uint32_t row_bytes)
+{
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) bytes += in[n] ? row_bytes : 0;
+    mbar_arrive_expect_tx(&r.full[stage], bytes);
+    uint8_t *dst = r.base + stage * r.stage_bytes;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (in[n]) {
+            bulk_load(dst, in[n] + row * row_bytes, row_bytes, &r.full[stage]);
+            dst += row_bytes;
+        }
+}
+
+// Waits for a stage; false if its copies have not landed within the limit (of a sound device
+// they always do), in which case the row's results are made NaN.
+__device__ __forceinline__ bool ring_wait(const Ring &r, int stage, uint32_t parity)
+{
+    return sm100::mbar_wait(&r.full[stage], parity, sm100::kWaitLimitCycles);
+}
+
+// The group's part of the block's dynamic shared memory: barriers first, then the stages.
+template <int W>
+__device__ __forceinline__ Ring ring_of(uint8_t *smem, int depth, int stage_bytes)
+{
+    constexpr int kGroups = NormShape<W>::kGroups;
+    const int group = threadIdx.x / (32 * W);
+    Ring r;
+    r.depth = depth;
+    r.stage_bytes = stage_bytes;
+    r.full = reinterpret_cast<uint64_t *>(smem) + group * kMaxRing;
+    r.base = smem + kGroups * kMaxRing * 8 + (int64_t)group * depth * stage_bytes;
+    return r;
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8_e4m3(uint8_t *row, int i, int width, const float (&f)[8])
+__device__ __forceinline__ void store8_e4m3(uint8_t *row, int c0, int width, const float (&f)[8])
 {
     if constexpr (VEC) {
+        const int i = elem8<true>(c0, 0);
         if (i >= width) return;
         uint32_t u[2];
 #pragma unroll
@@ -81,144 +156,251 @@ __device__ __forceinline__ void store8_e4m3(uint8_t *row, int i, int width, cons
         *reinterpret_cast<uint2 *>(row + i) = make_uint2(u[0], u[1]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (i + e < width) row[i + e] = __nv_cvt_float_to_fp8(f[e], __NV_SATFINITE, __NV_E4M3);
+        for (int e = 0; e < 8; ++e) {
+            const int i = elem8<false>(c0, e);
+            if (i < width) row[i] = __nv_cvt_float_to_fp8(f[e], __NV_SATFINITE, __NV_E4M3);
+        }
     }
 }
 
-template <int W> struct NormShape {
-    static constexpr int kWarps = W < 8 ? 8 : W;
-    static constexpr int kRows = kWarps / W;       // rows per block
-};
-
-template <typename T, int W, int NC, bool E4M3, bool VEC>
-__global__ void __launch_bounds__(32 * NormShape<W>::kWarps)
-    rms_norm_kernel(const __grid_constant__ RmsArgs a)
+// y * (448 / max) and the scales of one chunk of 256 columns from c0, in groups of `group`
+// columns (32, 64 or 128).  VEC: a group is group / 8 neighbouring lanes.  Otherwise it is
+// group / 32 elements of every lane.
+template <bool VEC>
+__device__ __forceinline__ void scale_groups(float (&h)[8], int c0, int width, int group,
+                                             float *scales)
 {
-    constexpr int kRows = NormShape<W>::kRows;
-    __shared__ float buf[2][NormShape<W>::kWarps];
-    const int t = threadIdx.x % (32 * W);
-    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (32 * W);
-    const bool live = row < a.rows;
-    const int width = live ? a.width : 0;
-    const int64_t base = live ? row * a.width : 0;
-    const T *x = reinterpret_cast<const T *>(a.x) + base;
-    const T *r = reinterpret_cast<const T *>(a.resid) + base;
-    float h[NC][8];
-    float ss = 0.f;
+    const int lane = threadIdx.x & 31;
+    if constexpr (VEC) {
+        float m = 0.f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) load8<VEC>(x, (c * 32 * W + t) * 8, width, h[c]);
-    if (a.resid) {
-        float b[NC][8];
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[e]));
+        for (int o = group / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+        m = scale_top(m);
+        const int i = elem8<true>(c0, 0);
+        if (i < width && i % group == 0) scales[i / group] = m * (1.f / kE4m3Max);
+        const float back = m > 0.f ? kE4m3Max / m : 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load8<VEC>(r, (c * 32 * W + t) * 8, width, b[c]);
+        for (int e = 0; e < 8; ++e) h[e] *= back;
+    } else {
+        const int per = group / 32;                    // 1, 2 or 4 elements
+        float m[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = fabsf(h[e]);
+        if (per > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) m[e] = m[e + 1] = fmaxf(m[e], m[e + 1]);
+        }
+        if (per > 2) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) m[e] = m[e + 1] = m[e + 2] = m[e + 3] = fmaxf(m[e], m[e + 2]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e % per == 0) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(kFullMask, m[e], o));
+                m[e] = scale_top(m[e]);
+                const int i = c0 + 32 * e;
+                if (lane == 0 && i < width) scales[i / group] = m[e] * (1.f / kE4m3Max);
+            } else {
+                m[e] = m[e - 1];
+            }
+            h[e] *= m[e] > 0.f ? kE4m3Max / m[e] : 0.f;
+        }
+    }
+}
+
+template <typename T, int W, bool E4M3, Access A>
+__global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBlocks)
+    rms_norm_kernel(const __grid_constant__ RmsArgs a, int depth)
+{
+    constexpr bool VEC = A != ELEMENTS;
+    constexpr int kGroups = NormShape<W>::kGroups;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float buf[2][NormShape<W>::kThreads / 32];
+    const int group = threadIdx.x / (32 * W), wg = (threadIdx.x / 32) % W;
+    const bool lead = threadIdx.x % (32 * W) == 0;
+    const int64_t stride = (int64_t)gridDim.x * kGroups;
+    int64_t row = (int64_t)blockIdx.x * kGroups + group;
+    const int width = a.width;
+    const uint32_t row_bytes = (uint32_t)width * sizeof(T);
+    const uint8_t *const in[2] = {reinterpret_cast<const uint8_t *>(a.x),
+                                  reinterpret_cast<const uint8_t *>(a.resid)};
+    Ring ring;
+    if constexpr (A == RING) {
+        ring = ring_of<W>(smem, depth, (a.resid ? 2 : 1) * row_bytes);
+        if (lead) {
+            for (int s = 0; s < depth; ++s) mbar_init(&ring.full[s], 1);
+            sm100::fence_mbar_init();
+        }
+        group_sync<W>();
+    }
+    grid_dep_wait();
+    grid_dep_release();
+    if (A == RING && lead)
+        for (int s = 0; s < depth && row + s * stride < a.rows; ++s)
+            ring_fill(ring, s, in, row + s * stride, row_bytes);
+    float w[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        if (a.weight) {
+            load8<VEC>(a.weight, (c * W + wg) * 256, width, w[c]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[c][e] = 1.f;
+        }
+    }
+    int stage = 0;
+    uint32_t parity = 0;
+    for (; row < a.rows; row += stride) {
+        const int64_t base = row * width;
+        const T *x = reinterpret_cast<const T *>(a.x) + base;
+        const T *r = a.resid ? reinterpret_cast<const T *>(a.resid) + base : nullptr;
+        bool landed = true;
+        if constexpr (A == RING) {
+            landed = ring_wait(ring, stage, parity);
+            x = reinterpret_cast<const T *>(ring.base + stage * ring.stage_bytes);
+            r = a.resid ? x + width : nullptr;
+        }
+        float h[NC][8];
+        float ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) load8<VEC>(x, (c * W + wg) * 256, width, h[c]);
+        if (r) {
+            float b[NC][8];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) load8<VEC>(r, (c * W + wg) * 256, width, b[c]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[c][e] += b[c][e];
+        }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] += b[c][e];
-    }
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
-    ss = group_sum<W>(ss, buf[0]);
-    const float rs = rsqrtf(ss / (float)a.width + a.eps);
-    if (a.rstd && live && t == 0) a.rstd[row] = rs;
-    if (a.sum) {
-        T *s = reinterpret_cast<T *>(a.sum) + base;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) store8<VEC>(s, (c * 32 * W + t) * 8, width, h[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        float w[8];
-        if (a.weight) load8<VEC>(a.weight, (c * 32 * W + t) * 8, width, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[c][e] = a.weight ? h[c][e] * rs * w[e] : h[c][e] * rs;
-    }
-    if constexpr (!E4M3) {
-        T *y = reinterpret_cast<T *>(a.y) + base;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) store8<VEC>(y, (c * 32 * W + t) * 8, width, h[c]);
-    } else {
-        uint8_t *y = reinterpret_cast<uint8_t *>(a.y) + base;
-        float m[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            m[c] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m[c] = fmaxf(m[c], fabsf(h[c][e]));
-        }
-        if (a.group == 0) {
-            float mm = m[0];
-#pragma unroll
-            for (int c = 1; c < NC; ++c) mm = fmaxf(mm, m[c]);
-            mm = scale_top(group_max<W>(mm, buf[1]));
-#pragma unroll
-            for (int c = 0; c < NC; ++c) m[c] = mm;
-            if (live && t == 0) a.scales[row] = mm * (1.f / kE4m3Max);
-        } else {
-            const int lanes = a.group / 8;              // 4, 8 or 16 neighbouring threads
-            const int groups = (a.width + a.group - 1) / a.group;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                for (int o = lanes / 2; o > 0; o >>= 1)
-                    m[c] = fmaxf(m[c], __shfl_xor_sync(kFullMask, m[c], o));
-                m[c] = scale_top(m[c]);
-                const int i = (c * 32 * W + t) * 8;
-                if (i < width && t % lanes == 0)
-                    a.scales[row * groups + i / a.group] = m[c] * (1.f / kE4m3Max);
+            for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
+        ss = group_reduce<W, false>(ss, buf[0]);
+        if constexpr (A == RING) {
+            // every thread of the group has read the stage
+            if constexpr (W == 1) __syncwarp();
+            if (lead && row + depth * stride < a.rows)
+                ring_fill(ring, stage, in, row + depth * stride, row_bytes);
+            if (++stage == depth) {
+                stage = 0;
+                parity ^= 1;
             }
         }
+        const float rs = landed ? rsqrtf(ss / (float)width + a.eps) : CUDART_NAN_F;
+        if (a.rstd && lead) a.rstd[row] = rs;
+        if (a.sum) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const float back = m[c] > 0.f ? kE4m3Max / m[c] : 0.f;
+            for (int c = 0; c < NC; ++c)
+                store8<VEC>(reinterpret_cast<T *>(a.sum) + base, (c * W + wg) * 256, width, h[c]);
+        }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] *= back;
-            store8_e4m3<VEC>(y, (c * 32 * W + t) * 8, width, h[c]);
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[c][e] *= rs * w[c][e];
+        if constexpr (!E4M3) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                store8<VEC>(reinterpret_cast<T *>(a.y) + base, (c * W + wg) * 256, width, h[c]);
+            if constexpr (W > 1) group_sync<W>();          // buf is used again
+        } else {
+            if (a.group == 0) {
+                float m = 0.f;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[c][e]));
+                m = scale_top(group_reduce<W, true>(m, buf[1]));
+                if (lead) a.scales[row] = m * (1.f / kE4m3Max);
+                const float back = m > 0.f ? kE4m3Max / m : 0.f;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[c][e] *= back;
+            } else {
+                const int groups = (width + a.group - 1) / a.group;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    scale_groups<VEC>(h[c], (c * W + wg) * 256, width, a.group, a.scales + row * groups);
+                if constexpr (W > 1) group_sync<W>();
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                store8_e4m3<VEC>(reinterpret_cast<uint8_t *>(a.y) + base, (c * W + wg) * 256, width, h[c]);
         }
     }
 }
 
-// Each block walks rows with a stride of the grid and keeps its columns' part of the weight
-// gradient in registers; the parts meet in shared memory and leave as one row of `part` per
-// block, which rms_dweight_kernel adds in a fixed order.
-template <typename T, int W, int NC, bool VEC>
-__global__ void __launch_bounds__(32 * NormShape<W>::kWarps)
-    rms_norm_bwd_kernel(const __grid_constant__ RmsBwdArgs a)
+// Each group walks rows with a stride of the grid and keeps its columns' part of the weight
+// gradient in registers; the parts of a block meet in shared memory and leave as one row of
+// `part`, which rms_dweight_kernel adds in a fixed order.
+template <typename T, int W, Access A>
+__global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBlocks)
+    rms_norm_bwd_kernel(const __grid_constant__ RmsBwdArgs a, int depth)
 {
-    constexpr int kRows = NormShape<W>::kRows;
-    constexpr int kWarps = NormShape<W>::kWarps;
-    __shared__ float buf[2][kWarps];
-    extern __shared__ float dws[];                      // [kRows][width] when kRows > 1
-    const int t = threadIdx.x % (32 * W);
-    const int sub = threadIdx.x / (32 * W);
+    constexpr bool VEC = A != ELEMENTS;
+    constexpr int kGroups = NormShape<W>::kGroups;
+    extern __shared__ __align__(128) uint8_t smem[];       // the ring, then [kGroups][width] floats
+    __shared__ float buf[2][NormShape<W>::kThreads / 32];
+    const int group = threadIdx.x / (32 * W), wg = (threadIdx.x / 32) % W;
+    const bool lead = threadIdx.x % (32 * W) == 0;
+    const int64_t stride = (int64_t)gridDim.x * kGroups;
+    int64_t row = (int64_t)blockIdx.x * kGroups + group;
+    const int width = a.width;
+    const uint32_t row_bytes = (uint32_t)width * sizeof(T);
+    const uint8_t *const in[3] = {reinterpret_cast<const uint8_t *>(a.dy),
+                                  reinterpret_cast<const uint8_t *>(a.h),
+                                  reinterpret_cast<const uint8_t *>(a.dsum)};
+    Ring ring;
+    if constexpr (A == RING) {
+        ring = ring_of<W>(smem, depth, (a.dsum ? 3 : 2) * row_bytes);
+        if (lead) {
+            for (int s = 0; s < depth; ++s) mbar_init(&ring.full[s], 1);
+            sm100::fence_mbar_init();
+        }
+        group_sync<W>();
+    }
+    grid_dep_wait();
+    grid_dep_release();
+    if (A == RING && lead)
+        for (int s = 0; s < depth && row + s * stride < a.rows; ++s)
+            ring_fill(ring, s, in, row + s * stride, row_bytes);
     float acc[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[c][e] = 0.f;
-    int parity = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows;
-         row0 += (int64_t)gridDim.x * kRows, parity ^= 1) {
-        const int64_t row = row0 + sub;
-        const bool live = row < a.rows;
-        const int width = live ? a.width : 0;
-        const int64_t base = live ? row * a.width : 0;
+    int stage = 0, flip = 0;
+    uint32_t parity = 0;
+    float rs_next = row < a.rows ? a.rstd[row] : 0.f;      // one row ahead
+    for (; row < a.rows; row += stride, flip ^= 1) {
+        const int64_t base = row * width;
         const T *dy = reinterpret_cast<const T *>(a.dy) + base;
         const T *hp = reinterpret_cast<const T *>(a.h) + base;
-        const float rs = live ? a.rstd[row] : 0.f;
+        const T *ds = a.dsum ? reinterpret_cast<const T *>(a.dsum) + base : nullptr;
+        float rs = rs_next;
+        if (row + stride < a.rows) rs_next = a.rstd[row + stride];
+        if constexpr (A == RING) {
+            if (!ring_wait(ring, stage, parity)) rs = CUDART_NAN_F;
+            dy = reinterpret_cast<const T *>(ring.base + stage * ring.stage_bytes);
+            hp = dy + width;
+            ds = a.dsum ? hp + width : nullptr;
+        }
         float g[NC][8], h[NC][8];
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            load8<VEC>(dy, (c * 32 * W + t) * 8, width, g[c]);
-            load8<VEC>(hp, (c * 32 * W + t) * 8, width, h[c]);
+            load8<VEC>(dy, (c * W + wg) * 256, width, g[c]);
+            load8<VEC>(hp, (c * W + wg) * 256, width, h[c]);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float w[8];
-            if (a.weight) load8<VEC>(a.weight, (c * 32 * W + t) * 8, width, w);
+            if (a.weight) load8<VEC>(a.weight, (c * W + wg) * 256, width, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 h[c][e] *= rs;
@@ -227,66 +409,74 @@ __global__ void __launch_bounds__(32 * NormShape<W>::kWarps)
                 dot = fmaf(g[c][e], h[c][e], dot);
             }
         }
-        dot = group_sum<W>(dot, buf[parity]) / (float)a.width;
+        dot = group_reduce<W, false>(dot, buf[flip]) / (float)width;
         T *dx = reinterpret_cast<T *>(a.dx) + base;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float o[8];
-            if (a.dsum)
-                load8<VEC>(reinterpret_cast<const T *>(a.dsum) + base, (c * 32 * W + t) * 8, width, o);
+            if (ds) load8<VEC>(ds, (c * W + wg) * 256, width, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float d = rs * (g[c][e] - h[c][e] * dot);
-                o[e] = a.dsum ? d + o[e] : d;
+                o[e] = ds ? d + o[e] : d;
             }
-            store8<VEC>(dx, (c * 32 * W + t) * 8, width, o);
+            store8<VEC>(dx, (c * W + wg) * 256, width, o);
+        }
+        if constexpr (A == RING) {
+            group_sync<W>();                               // the group has read the stage
+            if (lead && row + depth * stride < a.rows)
+                ring_fill(ring, stage, in, row + depth * stride, row_bytes);
+            if (++stage == depth) {
+                stage = 0;
+                parity ^= 1;
+            }
         }
     }
     if (!a.dweight) return;
-    float *part = a.part + (int64_t)blockIdx.x * a.width;
-    if constexpr (kRows == 1) {
+    float *part = a.part + (int64_t)blockIdx.x * width;
+    if constexpr (kGroups == 1) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) store8<VEC>(part, (c * 32 * W + t) * 8, a.width, acc[c]);
+        for (int c = 0; c < NC; ++c) store8<VEC>(part, (c * W + wg) * 256, width, acc[c]);
     } else {
+        // the groups' stages are done with: their memory holds the groups' parts
+        float *dws = reinterpret_cast<float *>(smem);
+        __syncthreads();
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            store8<VEC>(dws + sub * a.width, (c * 32 * W + t) * 8, a.width, acc[c]);
+            store8<VEC>(dws + group * width, (c * W + wg) * 256, width, acc[c]);
         __syncthreads();
-        for (int i = threadIdx.x; i < a.width; i += blockDim.x) {
+        for (int i = threadIdx.x; i < width; i += blockDim.x) {
             float s = 0.f;
 #pragma unroll
-            for (int q = 0; q < kRows; ++q) s += dws[q * a.width + i];
+            for (int q = 0; q < kGroups; ++q) s += dws[q * width + i];
             part[i] = s;
         }
     }
 }
 
-// dweight[i] = sum of the blocks' parts, in block order within each of 8 strands, the
+// dweight[i] = sum of the blocks' parts, in block order within each of 32 strands, the
 // strands in order: the same result every time.
-__global__ void __launch_bounds__(256) rms_dweight_kernel(const float *__restrict__ part,
-                                                          int blocks, int width,
-                                                          float *__restrict__ dweight)
+__global__ void __launch_bounds__(1024) rms_dweight_kernel(const float *__restrict__ part,
+                                                           int blocks, int width,
+                                                           float *__restrict__ dweight)
 {
-    __shared__ float s[8][32];
+    __shared__ float s[32][33];
     grid_dep_wait();
+    grid_dep_release();
     const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (i < width) {
-#pragma unroll 4
-        for (int b = strand; b < blocks; b += 8) v += part[(int64_t)b * width + i];
+#pragma unroll 10
+        for (int b = strand; b < blocks; b += 32) v += part[(int64_t)b * width + i];
     }
     s[strand][lane] = v;
     __syncthreads();
-    if (strand == 0 && i < width) {
-        float r = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) r += s[q][lane];
-        dweight[i] = r;
-    }
+    const float r = warp_sum(s[lane][strand]);             // column blockIdx.x * 32 + strand
+    if (lane == 0 && blockIdx.x * 32 + strand < width) dweight[blockIdx.x * 32 + strand] = r;
 }
 
-// Warps per row: two chunks of 8 elements per thread, so 512 columns per warp.
+// Warps per row: 512 columns per warp.
 int warps_for(int width)
 {
     int w = 1;
@@ -294,17 +484,37 @@ int warps_for(int width)
     return w;
 }
 
+// The ring's depth: as many stages as 160 KB per SM hold, 4 at most.
+template <int W>
+int ring_depth(int blocks_per_sm, int64_t stage_bytes)
+{
+    const int64_t groups = (int64_t)blocks_per_sm * NormShape<W>::kGroups;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRing, 160 * 1024 / (groups * stage_bytes)));
+}
+
+template <typename K, typename Args>
+cudaError_t launch_norm(K kern, const Args &a, int64_t blocks, int threads, size_t smem, int depth,
+                        cudaStream_t st)
+{
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)threads), smem, st, a, depth);
+}
+
 template <typename T, bool E4M3, int W>
 cudaError_t run_fwd(const RmsArgs &a, cudaStream_t st)
 {
-    constexpr int kRows = NormShape<W>::kRows;
-    const unsigned grid = (unsigned)((a.rows + kRows - 1) / kRows);
-    const unsigned thr = 32 * NormShape<W>::kWarps;
-    if (a.width % 8 == 0)
-        rms_norm_kernel<T, W, 2, E4M3, true><<<grid, thr, 0, st>>>(a);
-    else
-        rms_norm_kernel<T, W, 2, E4M3, false><<<grid, thr, 0, st>>>(a);
-    return cudaGetLastError();
+    using S = NormShape<W>;
+    const int64_t most = (int64_t)num_sms() * S::kFwdBlocks;
+    const int64_t blocks = (a.rows + S::kGroups - 1) / S::kGroups;
+    if (a.width % 8 != 0)
+        return launch_norm(rms_norm_kernel<T, W, E4M3, ELEMENTS>, a, blocks, S::kThreads, 0, 0, st);
+    if (blocks <= most)
+        return launch_norm(rms_norm_kernel<T, W, E4M3, DIRECT>, a, blocks, S::kThreads, 0, 0, st);
+    const int64_t stage = (int64_t)a.width * sizeof(T) * (a.resid ? 2 : 1);
+    const int depth = ring_depth<W>(S::kFwdBlocks, stage);
+    return launch_norm(rms_norm_kernel<T, W, E4M3, RING>, a, most, S::kThreads,
+                       S::kGroups * (kMaxRing * 8 + depth * stage), depth, st);
 }
 
 template <typename T, bool E4M3>
@@ -323,17 +533,23 @@ cudaError_t fwd_w(const RmsArgs &a, cudaStream_t st)
 template <typename T, int W>
 cudaError_t run_bwd(const RmsBwdArgs &a, cudaStream_t st)
 {
-    constexpr int kRows = NormShape<W>::kRows;
-    const unsigned thr = 32 * NormShape<W>::kWarps;
+    using S = NormShape<W>;
     const int blocks = rms_bwd_blocks(a.rows, a.width);
-    const size_t smem = kRows > 1 && a.dweight ? (size_t)kRows * a.width * 4 : 0;
-    if (a.width % 8 == 0)
-        rms_norm_bwd_kernel<T, W, 2, true><<<blocks, thr, smem, st>>>(a);
-    else
-        rms_norm_bwd_kernel<T, W, 2, false><<<blocks, thr, smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const size_t parts = S::kGroups > 1 && a.dweight ? (size_t)S::kGroups * a.width * 4 : 0;
+    cudaError_t e;
+    if (a.width % 8 != 0) {
+        e = launch_norm(rms_norm_bwd_kernel<T, W, ELEMENTS>, a, blocks, S::kThreads, parts, 0, st);
+    } else if (a.rows <= (int64_t)blocks * S::kGroups) {
+        e = launch_norm(rms_norm_bwd_kernel<T, W, DIRECT>, a, blocks, S::kThreads, parts, 0, st);
+    } else {
+        const int64_t stage = (int64_t)a.width * sizeof(T) * (a.dsum ? 3 : 2);
+        const int depth = ring_depth<W>(S::kBwdBlocks, stage);
+        e = launch_norm(rms_norm_bwd_kernel<T, W, RING>, a, blocks, S::kThreads,
+                        std::max(parts, (size_t)(S::kGroups * (kMaxRing * 8 + depth * stage))),
+                        depth, st);
+    }
     if (e != cudaSuccess || !a.dweight) return e;
-    return launch_pdl(rms_dweight_kernel, dim3((a.width + 31) / 32), dim3(256), 0, st,
+    return launch_pdl(rms_dweight_kernel, dim3((a.width + 31) / 32), dim3(1024), 0, st,
                       (const float *)a.part, blocks, a.width, a.dweight);
 }
 
@@ -354,10 +570,10 @@ cudaError_t bwd_w(const RmsBwdArgs &a, cudaStream_t st)
 
 int rms_bwd_blocks(int64_t rows, int width)
 {
+    // 512 threads per SM; more blocks would only add rows of partial sums
     const int w = warps_for(width), per = w < 8 ? 8 / w : 1;
-    const int64_t need = (rows + per - 1) / per;
-    const int64_t most = 296;
-    return (int)(need < 1 ? 1 : need < most ? need : most);
+    const int64_t need = (rows + per - 1) / per, most = w >= 16 ? 148 : 296;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(need, most));
 }
 
 cudaError_t launch_rms_norm(const RmsArgs &a, bool f32, bool e4m3, cudaStream_t st)
