@@ -55,6 +55,12 @@ __device__ __forceinline__ float scale_top(float m)
     return m > 0.f ? fmaxf(m, 7.888609e-31f /* 2^-100 */) : 0.f;
 }
 
+// 448 / m to 2 ulp (m is 0 or in the range of normal numbers).
+__device__ __forceinline__ float scale_back(float m)
+{
+    return m > 0.f ? __fdividef(kE4m3Max, m) : 0.f;
+}
+
 template <int W>
 __device__ __forceinline__ void group_sync()
 {
@@ -178,8 +184,9 @@ __device__ __forceinline__ void scale_groups(float (&h)[8], int c0, int width, i
         for (int o = group / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
         m = scale_top(m);
         const int i = elem8<true>(c0, 0);
-        if (i < width && i % group == 0) scales[i / group] = m * (1.f / kE4m3Max);
-        const float back = m > 0.f ? kE4m3Max / m : 0.f;
+        const int shift = 31 - __clz(group);           // a power of two
+        if (i < width && (i & (group - 1)) == 0) scales[i >> shift] = m * (1.f / kE4m3Max);
+        const float back = scale_back(m);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] *= back;
     } else {
@@ -206,7 +213,7 @@ __device__ __forceinline__ void scale_groups(float (&h)[8], int c0, int width, i
             } else {
                 m[e] = m[e - 1];
             }
-            h[e] *= m[e] > 0.f ? kE4m3Max / m[e] : 0.f;
+            h[e] *= scale_back(m[e]);
         }
     }
 }
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBloc
                     for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[c][e]));
                 m = scale_top(group_reduce<W, true>(m, buf[1]));
                 if (lead) a.scales[row] = m * (1.f / kE4m3Max);
-                const float back = m > 0.f ? kE4m3Max / m : 0.f;
+                const float back = scale_back(m);
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -369,11 +376,18 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
     if (A == RING && lead)
         for (int s = 0; s < depth && row + s * stride < a.rows; ++s)
             ring_fill(ring, s, in, row + s * stride, row_bytes);
-    float acc[NC][8];
+    // the weights stay in registers: with shared memory full of rows L1 keeps nothing, and
+    // reading them again for every row took 127 us instead of 83 (8192 x 8192 bf16)
+    float acc[NC][8], w[NC][8];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC; ++c) {
+        if (a.weight) load8<VEC>(a.weight, (c * W + wg) * 256, width, w[c]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[c][e] = 0.f;
+        for (int e = 0; e < 8; ++e) {
+            acc[c][e] = 0.f;
+            if (!a.weight) w[c][e] = 1.f;
+        }
+    }
     int stage = 0, flip = 0;
     uint32_t parity = 0;
     float rs_next = row < a.rows ? a.rstd[row] : 0.f;      // one row ahead
@@ -398,17 +412,14 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
             load8<VEC>(hp, (c * W + wg) * 256, width, h[c]);
         }
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float w[8];
-            if (a.weight) load8<VEC>(a.weight, (c * W + wg) * 256, width, w);
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 h[c][e] *= rs;
                 acc[c][e] = fmaf(g[c][e], h[c][e], acc[c][e]);
-                if (a.weight) g[c][e] *= w[e];
+                g[c][e] *= w[c][e];
                 dot = fmaf(g[c][e], h[c][e], dot);
             }
-        }
         dot = group_reduce<W, false>(dot, buf[flip]) / (float)width;
         T *dx = reinterpret_cast<T *>(a.dx) + base;
 #pragma unroll
@@ -484,12 +495,28 @@ int warps_for(int width)
     return w;
 }
 
-// The ring's depth: as many stages as 160 KB per SM hold, 4 at most.
+// How many blocks share an SM and how deep their rings are: rows in flight of `flight` bytes per
+// SM.  (Forward, 64 KB: 16384 x 4096 bf16 to e4m3 takes 75 us; with 128 KB in flight 82 and with
+// 192 KB 88, as reads that run further ahead only crowd the writes; with half the warps 91.)
+// The blocks' shared memory is sized to leave no room for more of them, or a kernel behind
+// this one would place its blocks unevenly.
+struct RingPlan {
+    int blocks, depth;
+    size_t smem;
+};
+
 template <int W>
-int ring_depth(int blocks_per_sm, int64_t stage_bytes)
+RingPlan ring_plan(int blocks, int64_t stage_bytes, int64_t flight)
 {
-    const int64_t groups = (int64_t)blocks_per_sm * NormShape<W>::kGroups;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRing, 160 * 1024 / (groups * stage_bytes)));
+    constexpr int64_t kSmem = 227 * 1024, kGroups = NormShape<W>::kGroups;
+    RingPlan p;
+    p.blocks = blocks;
+    while (p.blocks > 1 && p.blocks * kGroups * stage_bytes > flight) p.blocks /= 2;
+    const int64_t room = kSmem / p.blocks - 2048;
+    const int64_t most = std::min<int64_t>(kMaxRing, (room - kGroups * kMaxRing * 8) / (kGroups * stage_bytes));
+    p.depth = (int)std::max<int64_t>(1, std::min(most, flight / (p.blocks * kGroups * stage_bytes)));
+    p.smem = (size_t)room;
+    return p;
 }
 
 template <typename K, typename Args>
@@ -512,9 +539,9 @@ cudaError_t run_fwd(const RmsArgs &a, cudaStream_t st)
     if (blocks <= most)
         return launch_norm(rms_norm_kernel<T, W, E4M3, DIRECT>, a, blocks, S::kThreads, 0, 0, st);
     const int64_t stage = (int64_t)a.width * sizeof(T) * (a.resid ? 2 : 1);
-    const int depth = ring_depth<W>(S::kFwdBlocks, stage);
-    return launch_norm(rms_norm_kernel<T, W, E4M3, RING>, a, most, S::kThreads,
-                       S::kGroups * (kMaxRing * 8 + depth * stage), depth, st);
+    const RingPlan p = ring_plan<W>(S::kFwdBlocks, stage, 64 * 1024);
+    return launch_norm(rms_norm_kernel<T, W, E4M3, RING>, a, (int64_t)num_sms() * p.blocks,
+                       S::kThreads, p.smem, p.depth, st);
 }
 
 template <typename T, bool E4M3>
@@ -543,10 +570,8 @@ cudaError_t run_bwd(const RmsBwdArgs &a, cudaStream_t st)
         e = launch_norm(rms_norm_bwd_kernel<T, W, DIRECT>, a, blocks, S::kThreads, parts, 0, st);
     } else {
         const int64_t stage = (int64_t)a.width * sizeof(T) * (a.dsum ? 3 : 2);
-        const int depth = ring_depth<W>(S::kBwdBlocks, stage);
-        e = launch_norm(rms_norm_bwd_kernel<T, W, RING>, a, blocks, S::kThreads,
-                        std::max(parts, (size_t)(S::kGroups * (kMaxRing * 8 + depth * stage))),
-                        depth, st);
+        const RingPlan p = ring_plan<W>(S::kBwdBlocks, stage, 160 * 1024);
+        e = launch_norm(rms_norm_bwd_kernel<T, W, RING>, a, blocks, S::kThreads, p.smem, p.depth, st);
     }
     if (e != cudaSuccess || !a.dweight) return e;
     return launch_pdl(rms_dweight_kernel, dim3((a.width + 31) / 32), dim3(1024), 0, st,
