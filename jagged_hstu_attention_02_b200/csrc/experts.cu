@@ -27,8 +27,9 @@ namespace {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortOneBlock = 8192;     // pairs that one block sorts by itself
+constexpr int kSortOneBlock = 2048;     // pairs that one block sorts by itself
 constexpr int kSortMaxBlocks = 148;
+constexpr int kBatch = 4;               // ids per lane fetched at a time
 
 // The expert of pair p, or -1 (reported when the id is not below `experts`).
 template <typename I>
@@ -51,19 +52,36 @@ __device__ __forceinline__ void warp_run(int64_t lo, int64_t hi, int warp, int64
     e = min(hi, b + per);
 }
 
+// Calls f(pair, expert or -1) for the pairs [b, e) of this warp, 32 at a time and in order, all
+// lanes together; the ids of kBatch steps are fetched at once.
+template <typename I, typename F>
+__device__ __forceinline__ void walk_run(const SortArgs &a, int64_t b, int64_t e, bool report, F f)
+{
+    const int lane = threadIdx.x & 31;
+    for (int64_t p0 = b; p0 < e; p0 += 32 * kBatch) {
+        int x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t p = p0 + 32 * u + lane;
+            x[u] = p < e ? expert_of<I>(a, p, report) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (p0 + 32 * u < e) f(p0 + 32 * u + lane, x[u]);       // (warp-uniform)
+    }
+}
+
 // Counts this warp's pairs per expert into its own row of shared memory.
 template <typename I>
 __device__ __forceinline__ void count_run(const SortArgs &a, int64_t b, int64_t e, int32_t *mine,
                                           bool report)
 {
     const int lane = threadIdx.x & 31;
-    for (int64_t p0 = b; p0 < e; p0 += 32) {
-        const int64_t p = p0 + lane;
-        const int x = p < e ? expert_of<I>(a, p, report) : -1;
+    walk_run<I>(a, b, e, report, [&](int64_t, int x) {
         const unsigned same = __match_any_sync(kFullMask, x);
         if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
         __syncwarp();
-    }
+    });
 }
 
 // Exclusive prefix sum over the block's threads of one value each; *total their sum.
@@ -95,9 +113,7 @@ template <typename I>
 __device__ __forceinline__ void place_run(const SortArgs &a, int64_t b, int64_t e, int32_t *mine)
 {
     const int lane = threadIdx.x & 31;
-    for (int64_t p0 = b; p0 < e; p0 += 32) {
-        const int64_t p = p0 + lane;
-        const int x = p < e ? expert_of<I>(a, p, false) : -1;
+    walk_run<I>(a, b, e, false, [&](int64_t p, int x) {
         const unsigned same = __match_any_sync(kFullMask, x);
         int at = -1;
         if (x >= 0) at = mine[x] + __popc(same & ((1u << lane) - 1u));
@@ -108,7 +124,7 @@ __device__ __forceinline__ void place_run(const SortArgs &a, int64_t b, int64_t 
             a.slots[p] = at;
             if (at >= 0 && a.rows) a.rows[at] = p / a.choices;
         }
-    }
+    });
 }
 
 // ONE: the whole sort in one block.  Otherwise the second launch of two: expert_count_kernel
@@ -118,15 +134,44 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid
 {
     extern __shared__ int32_t sh[];                  // [kSortWarps][experts]
     __shared__ int wsum[kSortWarps];
-    const int tid = threadIdx.x, warp = tid >> 5;
+    __shared__ int32_t sums[2][ONE ? 1 : kMaxExperts];   // pairs of all blocks, of earlier blocks
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t chunk = (a.n + gridDim.x - 1) / gridDim.x;
     const int64_t lo = min(a.n, (int64_t)blockIdx.x * chunk), hi = min(a.n, lo + chunk);
     int64_t b, e;
     warp_run(lo, hi, warp, b, e);
     for (int x = tid; x < kSortWarps * a.experts; x += kSortThreads) sh[x] = 0;
+    if constexpr (ONE) {
+        grid_dep_wait();
+        grid_dep_release();
+    }
     __syncthreads();
     count_run<I>(a, b, e, sh + warp * a.experts, ONE);
-    if constexpr (!ONE) grid_dep_wait();
+    if constexpr (!ONE) {
+        // the blocks' counts: 32 experts and a share of the blocks per warp
+        for (int x = tid; x < a.experts; x += kSortThreads) sums[0][x] = sums[1][x] = 0;
+        grid_dep_wait();
+        grid_dep_release();
+        __syncthreads();
+        const int chunks = (a.experts + 31) / 32;
+        const int shares = chunks >= kSortWarps ? 1 : kSortWarps / chunks;
+        const int per = ((int)gridDim.x + shares - 1) / shares;
+        for (int task = warp; task < chunks * shares; task += kSortWarps) {
+            const int x = task % chunks * 32 + lane, q0 = task / chunks * per;
+            const int q1 = min(q0 + per, (int)gridDim.x);
+            int all = 0, before = 0;
+            if (x < a.experts) {
+#pragma unroll 16
+                for (int q = q0; q < q1; ++q) {
+                    const int v = a.hist[(int64_t)q * a.experts + x];
+                    all += v;
+                    if (q < (int)blockIdx.x) before += v;
+                }
+                atomicAdd(&sums[0][x], all);
+                atomicAdd(&sums[1][x], before);
+            }
+        }
+    }
     __syncthreads();
     int base = 0;
     for (int x0 = 0; x0 < a.experts; x0 += kSortThreads) {
@@ -136,12 +181,8 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid
             if constexpr (ONE) {
                 for (int w = 0; w < kSortWarps; ++w) all += sh[w * a.experts + x];
             } else {
-#pragma unroll 8
-                for (int q = 0; q < (int)gridDim.x; ++q) {
-                    const int v = a.hist[(int64_t)q * a.experts + x];
-                    all += v;
-                    if (q < (int)blockIdx.x) before += v;
-                }
+                all = sums[0][x];
+                before = sums[1][x];
             }
         }
         int total;
@@ -171,6 +212,7 @@ __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid
     const int64_t lo = min(a.n, (int64_t)blockIdx.x * chunk), hi = min(a.n, lo + chunk);
     int64_t b, e;
     warp_run(lo, hi, warp, b, e);
+    grid_dep_wait();
     grid_dep_release();
     for (int x = tid; x < kSortWarps * a.experts; x += kSortThreads) sh[x] = 0;
     __syncthreads();
@@ -193,14 +235,12 @@ cudaError_t run_sort(const SortArgs &a, cudaStream_t st)
         auto k = expert_place_kernel<I, true>;
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        k<<<1, kSortThreads, smem, st>>>(a);
-        return cudaGetLastError();
+        return launch_pdl(k, dim3(1), dim3(kSortThreads), smem, st, a);
     }
     auto c = expert_count_kernel<I>;
     e = cudaFuncSetAttribute(c, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    c<<<blocks, kSortThreads, smem, st>>>(a);
-    e = cudaGetLastError();
+    e = launch_pdl(c, dim3(blocks), dim3(kSortThreads), smem, st, a);
     if (e != cudaSuccess) return e;
     auto k = expert_place_kernel<I, false>;
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -210,38 +250,33 @@ cudaError_t run_sort(const SortArgs &a, cudaStream_t st)
 
 // ------------------------------------------------------------------ rows of tokens
 
-// Warps that share a token's row, and tokens per block, for rows of `chunks` 16-byte (or
-// smaller) pieces: up to 4 pieces per thread, up to 8 warps.
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 8;            // per block
 
-int warps_per_row(int64_t chunks)
+// Warps that share a token's row of `pieces` pieces, `per_lane` of them per lane.
+int warps_per_row(int64_t pieces, int per_lane)
 {
     int w = 1;
-    while (w < kRowWarps && w * 128 < chunks) w *= 2;
+    while (w < kRowWarps && w * 32 * per_lane < pieces) w *= 2;
     return w;
 }
 
-// A row's slots in the lanes of a warp: lane j holds slot j (-1 where there is none).
-__device__ __forceinline__ int lane_slot(const int32_t *slots, int64_t t, int k, int64_t max_rows)
-{
-    const int lane = threadIdx.x & 31;
-    int s = lane < k ? slots[t * k + lane] : -1;
-    return s >= 0 && s < max_rows ? s : -1;
-}
-
-template <typename V>
+// Rows wider than 16 pieces: wpr warps per token read its row once, 4 pieces per lane in
+// flight, and write it to each of the token's places.
 __global__ void __launch_bounds__(32 * kRowWarps)
     expert_dispatch_kernel(const __grid_constant__ DispatchArgs a, int wpr)
 {
+    grid_dep_wait();
+    grid_dep_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kRowWarps / wpr) + warp / wpr;
     if (t >= a.tokens) return;
     const int part = warp % wpr;
-    const int mine = lane_slot(a.slots, t, a.choices, a.max_rows);
-    const int64_t per = a.row_bytes / (int64_t)sizeof(V);
-    const V *src = reinterpret_cast<const V *>(a.x + t * a.row_bytes);
+    int mine = lane < a.choices ? a.slots[t * a.choices + lane] : -1;
+    if (mine >= a.max_rows) mine = -1;
+    const int64_t per = a.row_bytes / 16;
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.x + t * a.row_bytes);
     for (int64_t c0 = part * 32 + lane; c0 - lane < per; c0 += 4 * 32 * wpr) {
-        V v[4];
+        uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int64_t c = c0 + u * 32 * wpr;
@@ -250,7 +285,7 @@ __global__ void __launch_bounds__(32 * kRowWarps)
         for (int j = 0; j < a.choices; ++j) {
             const int s = __shfl_sync(kFullMask, mine, j);
             if (s < 0) continue;
-            V *dst = reinterpret_cast<V *>(a.out + (int64_t)s * a.row_bytes);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)s * a.row_bytes);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int64_t c = c0 + u * 32 * wpr;
@@ -267,127 +302,413 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     }
 }
 
-template <typename T, bool VEC>
+// The same for rows that start anywhere (row_bytes no multiple of 16), 512 bytes per warp and
+// turn, the token's row put together for each of its places as that place lies; ES: the bytes
+// that a row's ends are cut to.
+template <int ES>
 __global__ void __launch_bounds__(32 * kRowWarps)
-    expert_combine_kernel(const __grid_constant__ CombineArgs a, int wpr)
+    expert_dispatch_shifted_kernel(const __grid_constant__ DispatchArgs a, int wpr)
 {
+    grid_dep_wait();
+    grid_dep_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kRowWarps / wpr) + warp / wpr;
     if (t >= a.tokens) return;
-    const int mine = lane_slot(a.slots, t, a.choices, a.max_rows);
-    float weight = 1.f;
-    if (a.weights && lane < a.choices) weight = a.weights[t * a.choices + lane];
-    const T *y = reinterpret_cast<const T *>(a.y);
-    for (int i0 = (warp % wpr) * 256; i0 < a.width; i0 += 256 * wpr) {
-        float acc[8];
-        if (a.resid) {
-            load8<VEC>(reinterpret_cast<const T *>(a.resid) + t * a.width, i0, a.width, acc);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    const int part = warp % wpr;
+    int mine = lane < a.choices ? a.slots[t * a.choices + lane] : -1;
+    if (mine >= a.max_rows) mine = -1;
+    const uint8_t *src = a.x + t * a.row_bytes, *end = a.x + a.tokens * a.row_bytes;
+    for (int j = 0; j < a.choices; ++j) {
+        const int s = __shfl_sync(kFullMask, mine, j);
+        if (s < 0) continue;
+        uint8_t *dst = a.out + (int64_t)s * a.row_bytes;
+        const int lead = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
+        for (int64_t c0 = part * 512 - lead; c0 < a.row_bytes; c0 += 512 * wpr) {
+            uint32_t v[4];
+            load_words<4>(src + c0, src, src + a.row_bytes, a.x, end, v);
+            store_words<4, ES>(dst + c0, dst, dst + a.row_bytes, v);
         }
-        for (int j0 = 0; j0 < a.choices; j0 += 4) {
-            float f[4][8];
+    }
+    if (part != 0 || !a.scales) return;
+    for (int j = 0; j < a.choices; ++j) {
+        const int s = __shfl_sync(kFullMask, mine, j);
+        if (s < 0) continue;
+        for (int g = lane; g < a.n_scales; g += 32)
+            a.scales_out[(int64_t)s * a.n_scales + g] = a.scales[t * a.n_scales + g];
+    }
+}
+
+// Narrow rows: 2^shift lanes per (token, choice) pair, one piece each, so that a warp moves
+// several pairs (131072 tokens of 32 bytes, 8 choices: 96 us with a warp per token).
+template <typename V>
+__global__ void __launch_bounds__(256)
+    expert_dispatch_narrow_kernel(const __grid_constant__ DispatchArgs a, int shift)
+{
+    grid_dep_wait();
+    grid_dep_release();
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t pair = id >> shift;
+    if (pair >= a.tokens * a.choices) return;
+    const int c = (int)(id & ((1 << shift) - 1)), lanes = 1 << shift;
+    const int per = (int)(a.row_bytes / (int64_t)sizeof(V));
+    const int s = a.slots[pair];
+    if (s < 0 || s >= a.max_rows) return;
+    const int64_t t = (uint32_t)pair / (uint32_t)a.choices;        // tokens * choices < 2^31
+    if (c < per)
+        reinterpret_cast<V *>(a.out + (int64_t)s * a.row_bytes)[c] =
+            reinterpret_cast<const V *>(a.x + t * a.row_bytes)[c];
+    if (a.scales)
+        for (int g = c; g < a.n_scales; g += lanes)
+            a.scales_out[(int64_t)s * a.n_scales + g] = a.scales[t * a.n_scales + g];
+}
+
+template <typename V>
+cudaError_t run_dispatch(const DispatchArgs &a, cudaStream_t st)
+{
+    const int64_t per = a.row_bytes / (int64_t)sizeof(V);
+    if (per <= 16) {
+        int shift = 0;
+        while ((1 << shift) < per) ++shift;
+        const int64_t threads = (a.tokens * a.choices) << shift;
+        return launch_pdl(expert_dispatch_narrow_kernel<V>, dim3((unsigned)((threads + 255) / 256)),
+                          dim3(256), 0, st, a, shift);
+    }
+    const int wpr = warps_per_row((a.row_bytes + 15) / 16, sizeof(V) == 16 ? 4 : 1);
+    const int tokens = kRowWarps / wpr;
+    auto k = sizeof(V) == 16 ? expert_dispatch_kernel
+             : sizeof(V) == 1 ? expert_dispatch_shifted_kernel<1> : expert_dispatch_shifted_kernel<2>;
+    return launch_pdl(k, dim3((unsigned)((a.tokens + tokens - 1) / tokens)), dim3(32 * kRowWarps), 0,
+                      st, a, wpr);
+}
+
+// How a token's lanes lie, for the combine kernels.  Wide rows: wpr warps per token, 256
+// elements per warp and turn.  Narrow rows (VEC, at most 128 elements): lanes = 2^k >= width / 8
+// neighbours per token and 32 / lanes tokens per warp.
+struct RowLanes {
+    int wpr, lanes;
+};
+
+// A lane's part in a block's `tile` of tokens.
+struct TokenPart {
+    int64_t t;
+    int c0, step;              // first element of the warp's turns (wide), their distance
+    int lane;                  // among the token's lanes of this warp
+};
+
+__device__ __forceinline__ int tokens_per_tile(const RowLanes &r)
+{
+    return kRowWarps / r.wpr * (32 / r.lanes);
+}
+
+__device__ __forceinline__ TokenPart token_part(const RowLanes &r, int64_t tile)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    TokenPart p;
+    p.t = tile * tokens_per_tile(r) + (r.lanes == 32 ? warp / r.wpr : (warp * 32 + lane) / r.lanes);
+    p.c0 = r.lanes == 32 ? warp % r.wpr * 256 : 0;
+    p.step = 256 * r.wpr;
+    p.lane = lane & (r.lanes - 1);
+    return p;
+}
+
+// A token's places (-1: none) and weights.
+template <int KM>
+struct Places {
+    int s[KM];
+    float w[KM];
+    __device__ __forceinline__ void load(const CombineArgs &a, int64_t t)
+    {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                // lanes from `choices` up hold -1
-                const int s = __shfl_sync(kFullMask, mine, j0 + u);
-                load8<VEC>(y + (s < 0 ? 0 : (int64_t)s * a.width), i0, s < 0 ? 0 : a.width, f[u]);
+        for (int j = 0; j < KM; ++j) {
+            const bool has = t < a.tokens && j < a.choices;
+            s[j] = has ? a.slots[t * a.choices + j] : -1;
+            w[j] = a.weights && has ? a.weights[t * a.choices + j] : 1.f;
+        }
+    }
+    // Pairs without a row weigh 0, so that their (zero) rows may be added like the others': a
+    // branch around each pair's use pulled its fetch in too, one latency after another.
+    __device__ __forceinline__ void clip(int64_t max_rows)
+    {
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+            if (s[j] < 0 || s[j] >= max_rows) {
+                s[j] = -1;
+                w[j] = 0.f;
             }
+    }
+    // Row of pair j, and how much of it there is to read.
+    __device__ __forceinline__ int64_t row(int j) const { return s[j] < 0 ? 0 : s[j]; }
+    __device__ __forceinline__ int width(int j, int width) const { return s[j] < 0 ? 0 : width; }
+};
+
+// A narrow row's lanes may start anywhere in the warp: the c0 that makes elem8 count from them.
+__device__ __forceinline__ int lane_c0(int c0, int lane) { return c0 + 8 * (lane - (int)(threadIdx.x & 31)); }
+
+// Blocks per SM, so that the pieces of 4 choices fit the registers (fp32 takes twice as many).
+template <typename T, int KM>
+constexpr int combine_blocks()
+{
+    return sizeof(T) == 2 ? (KM <= 4 ? 4 : KM <= 8 ? 3 : 2) : KM <= 4 ? 3 : 2;
+}
+
+// KM: the choices, rounded up to a power of two.  Blocks stay and walk the tokens; the places
+// and weights of the next token are fetched while this one's rows move, and the rows of 4
+// choices before the first of them is used.
+template <typename T, int KM>
+__global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM>())
+    expert_combine_kernel(const __grid_constant__ CombineArgs a, const RowLanes r)
+{
+    constexpr int KB = KM < 4 ? KM : 4;
+    grid_dep_wait();
+    grid_dep_release();
+    const T *y = reinterpret_cast<const T *>(a.y), *y_end = y + a.max_rows * a.width;   // rows
+    const T *resid = reinterpret_cast<const T *>(a.resid), *r_end = resid + a.tokens * a.width;
+    const int per = tokens_per_tile(r);
+    Places<KM> now, next;
+    next.load(a, token_part(r, blockIdx.x).t);
+    for (int64_t tile = blockIdx.x; tile * per < a.tokens; tile += gridDim.x) {
+        const TokenPart p = token_part(r, tile);
+        now = next;
+        now.clip(a.max_rows);
+        next.load(a, token_part(r, tile + gridDim.x).t);
+        if (p.t >= a.tokens) continue;
+        T *out = reinterpret_cast<T *>(a.out) + p.t * a.width;
+        for (int turn = p.c0; turn < a.width; turn += p.step) {
+            const int c0 = lane_c0(turn, p.lane);
+            float acc[8];
+            Piece<T, true> first, f[KB];
+            if (resid) first.load(resid + p.t * a.width, c0, a.width, resid, r_end);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int s = __shfl_sync(kFullMask, mine, j0 + u);
-                const float w = __shfl_sync(kFullMask, weight, j0 + u);
-                if (s >= 0) {
+            for (int j0 = 0; j0 < KM; j0 += KB) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, f[u][e], acc[e]);
+                for (int u = 0; u < KB; ++u)
+                    f[u].load(y + now.row(j0 + u) * a.width, c0, now.width(j0 + u, a.width), y, y_end);
+                if (j0 == 0) {
+                    if (resid) {
+                        first.get(acc);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < KB; ++u) {
+                    float v[8];
+                    f[u].get(v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(now.w[j0 + u], v[e], acc[e]);
+                }
+            }
+            store8<true>(out, c0, a.width, acc);
+        }
+    }
+}
+
+template <typename T, int KM>
+__global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM>())
+    expert_combine_bwd_kernel(const __grid_constant__ CombineArgs a, const RowLanes r)
+{
+    constexpr int KB = KM < 4 ? KM : 4;
+    __shared__ float dots[2][kRowWarps][KM];
+    grid_dep_wait();
+    grid_dep_release();
+    const T *y = reinterpret_cast<const T *>(a.y), *y_end = y + a.max_rows * a.width;
+    const T *g_end = reinterpret_cast<const T *>(a.dout) + a.tokens * a.width;
+    T *dy = reinterpret_cast<T *>(a.dy);
+    const int warp = threadIdx.x >> 5, per = tokens_per_tile(r);
+    int flip = 0;
+    Places<KM> now, next;
+    next.load(a, token_part(r, blockIdx.x).t);
+    for (int64_t tile = blockIdx.x; tile * per < a.tokens; tile += gridDim.x, flip ^= 1) {
+        const TokenPart p = token_part(r, tile);
+        now = next;
+        now.clip(a.max_rows);
+        next.load(a, token_part(r, tile + gridDim.x).t);
+        const bool live = p.t < a.tokens;
+        const int width = live ? a.width : 0;
+        const T *dout = reinterpret_cast<const T *>(a.dout) + (live ? p.t * a.width : 0);
+        float dot[KM];
+#pragma unroll
+        for (int j = 0; j < KM; ++j) dot[j] = 0.f;
+        for (int turn = p.c0; turn < width; turn += p.step) {
+            const int c0 = lane_c0(turn, p.lane);
+            Piece<T, true> first, f[KB];
+            float g[8];
+            first.load(dout, c0, width, dout, g_end);
+#pragma unroll
+            for (int j0 = 0; j0 < KM; j0 += KB) {
+                if (a.dweights) {
+#pragma unroll
+                    for (int u = 0; u < KB; ++u)
+                        f[u].load(y + now.row(j0 + u) * a.width, c0, now.width(j0 + u, width), y, y_end);
+                }
+                if (j0 == 0) first.get(g);
+#pragma unroll
+                for (int u = 0; u < KB; ++u) {
+                    const int j = j0 + u;
+                    if (a.dweights) {
+                        float v[8];
+                        f[u].get(v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dot[j] = fmaf(g[e], v[e], dot[j]);
+                    }
+                    if (now.s[j] < 0) continue;
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = now.w[j] * g[e];
+                    store8<true>(dy + (int64_t)now.s[j] * a.width, c0, width, o);
                 }
             }
         }
-        store8<VEC>(reinterpret_cast<T *>(a.out) + t * a.width, i0, a.width, acc);
+        if (!a.dweights) continue;
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+            for (int o = r.lanes / 2; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(kFullMask, dot[j], o);
+        // (0 where a pair has no place)
+        if (r.wpr == 1) {
+            if (live && p.lane == 0) {
+#pragma unroll
+                for (int j = 0; j < KM; ++j)
+                    if (j < a.choices) a.dweights[p.t * a.choices + j] = dot[j];
+            }
+        } else {
+            if (p.lane == 0) {
+#pragma unroll
+                for (int j = 0; j < KM; ++j) dots[flip][warp][j] = dot[j];
+            }
+            __syncthreads();
+            if (live && warp % r.wpr == 0 && p.lane < a.choices) {
+                float sum = 0.f;
+                for (int q = 0; q < r.wpr; ++q) sum += dots[flip][warp + q][p.lane];
+                a.dweights[p.t * a.choices + p.lane] = sum;
+            }
+        }
     }
 }
 
-// KM: the choices, rounded up to a power of two (their dot products stay in registers).
-template <typename T, bool VEC, int KM>
-__global__ void __launch_bounds__(32 * kRowWarps)
-    expert_combine_bwd_kernel(const __grid_constant__ CombineArgs a, int wpr)
+// The same for rows that start anywhere: wpr warps per token, a pair at a time, its row put
+// together as the row that is written lies (the token's forward, the pair's own backward).
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps, 5)
+    expert_combine_shifted_kernel(const __grid_constant__ CombineArgs a, int wpr)
 {
-    __shared__ float dots[kRowWarps][KM];
+    grid_dep_wait();
+    grid_dep_release();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (kRowWarps / wpr) + warp / wpr;
+    if (t >= a.tokens) return;
+    int place = lane < a.choices ? a.slots[t * a.choices + lane] : -1;
+    if (place >= a.max_rows) place = -1;
+    const float weight = a.weights && lane < a.choices ? a.weights[t * a.choices + lane] : 1.f;
+    const int width = a.width;
+    const T *y = reinterpret_cast<const T *>(a.y), *y_end = y + a.max_rows * width;
+    const T *resid = reinterpret_cast<const T *>(a.resid), *r_end = resid + a.tokens * width;
+    for (int c0 = warp % wpr * 256 - lead_of<false>(t, width); c0 < width; c0 += 256 * wpr) {
+        float acc[8] = {};
+        if (resid) load8<false>(resid + t * width, c0, width, resid, r_end, acc);
+        for (int j = 0; j < a.choices; ++j) {
+            const int s = __shfl_sync(kFullMask, place, j);
+            const float w = __shfl_sync(kFullMask, weight, j);
+            if (s < 0) continue;                           // (warp-uniform)
+            float v[8];
+            load8<false>(y + (int64_t)s * width, c0, width, y, y_end, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        }
+        store8<false>(reinterpret_cast<T *>(a.out) + t * width, c0, width, acc);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps, 5)
+    expert_combine_bwd_shifted_kernel(const __grid_constant__ CombineArgs a, int wpr)
+{
+    __shared__ float dots[kRowWarps][kMaxChoices];
+    grid_dep_wait();
+    grid_dep_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kRowWarps / wpr) + warp / wpr;
     const bool live = t < a.tokens;
-    const int mine = live ? lane_slot(a.slots, t, a.choices, a.max_rows) : -1;
-    float weight = 1.f;
-    if (a.weights && live && lane < a.choices) weight = a.weights[t * a.choices + lane];
-    const T *y = reinterpret_cast<const T *>(a.y);
+    int place = live && lane < a.choices ? a.slots[t * a.choices + lane] : -1;
+    if (place >= a.max_rows) place = -1;
+    const float weight = a.weights && live && lane < a.choices ? a.weights[t * a.choices + lane] : 1.f;
+    const int width = a.width;
+    const T *y = reinterpret_cast<const T *>(a.y), *y_end = y + a.max_rows * width;
+    const T *dout = reinterpret_cast<const T *>(a.dout), *g_end = dout + a.tokens * width;
     T *dy = reinterpret_cast<T *>(a.dy);
-    const int width = live ? a.width : 0;
-    float dot[KM];
-#pragma unroll
-    for (int j = 0; j < KM; ++j) dot[j] = 0.f;
-    for (int i0 = (warp % wpr) * 256; i0 < width; i0 += 256 * wpr) {
-        float g[8];
-        load8<VEC>(reinterpret_cast<const T *>(a.dout) + t * a.width, i0, width, g);
-#pragma unroll
-        for (int j = 0; j < KM; ++j) {
-            const int s = __shfl_sync(kFullMask, mine, j);
-            const float w = __shfl_sync(kFullMask, weight, j);
-            if (s < 0) continue;                       // (warp-uniform)
+    float mine = 0.f;                                      // lane j: the dot product of pair j
+    for (int j = 0; j < a.choices; ++j) {
+        const int s = __shfl_sync(kFullMask, place, j);
+        const float w = __shfl_sync(kFullMask, weight, j);
+        if (s < 0) continue;                               // (warp-uniform)
+        float d = 0.f;
+        for (int c0 = warp % wpr * 256 - lead_of<false>(s, width); c0 < width; c0 += 256 * wpr) {
+            float g[8], o[8];
+            load8<false>(dout + t * width, c0, width, dout, g_end, g);
             if (a.dweights) {
-                float f[8];
-                load8<VEC>(y + (int64_t)s * a.width, i0, width, f);
+                float v[8];
+                load8<false>(y + (int64_t)s * width, c0, width, y, y_end, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dot[j] = fmaf(g[e], f[e], dot[j]);
+                for (int e = 0; e < 8; ++e) d = fmaf(g[e], v[e], d);
             }
-            float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = w * g[e];
-            store8<VEC>(dy + (int64_t)s * a.width, i0, width, o);
+            store8<false>(dy + (int64_t)s * width, c0, width, o);
         }
+        d = warp_sum(d);
+        if (lane == j) mine = d;
     }
     if (!a.dweights) return;
-#pragma unroll
-    for (int j = 0; j < KM; ++j) dot[j] = warp_sum(dot[j]);
-    if (lane == 0) {
-#pragma unroll
-        for (int j = 0; j < KM; ++j) dots[warp][j] = dot[j];
-    }
+    if (lane < a.choices) dots[warp][lane] = mine;
     __syncthreads();
     if (live && warp % wpr == 0 && lane < a.choices) {
-        float s = 0.f;
-        for (int q = 0; q < wpr; ++q) s += dots[warp + q][lane];
-        a.dweights[t * a.choices + lane] = s;          // 0 where the pair has no place
+        float sum = 0.f;
+        for (int q = 0; q < wpr; ++q) sum += dots[warp + q][lane];
+        a.dweights[t * a.choices + lane] = sum;            // (0 where the pair has no place)
     }
 }
 
-template <typename T, bool VEC>
-cudaError_t run_combine_bwd(const CombineArgs &a, unsigned grid, int wpr, cudaStream_t st)
+template <typename T, int KM, bool BWD>
+cudaError_t run_combine_km(const CombineArgs &a, int64_t tiles, const RowLanes &r, cudaStream_t st)
 {
-    if (a.choices <= 1) expert_combine_bwd_kernel<T, VEC, 1><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr);
-    else if (a.choices <= 2) expert_combine_bwd_kernel<T, VEC, 2><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr);
-    else if (a.choices <= 4) expert_combine_bwd_kernel<T, VEC, 4><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr);
-    else if (a.choices <= 8) expert_combine_bwd_kernel<T, VEC, 8><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr);
-    else expert_combine_bwd_kernel<T, VEC, 16><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr);
-    return cudaGetLastError();
+    const int64_t most = (int64_t)num_sms() * combine_blocks<T, KM>();
+    const unsigned grid = (unsigned)(tiles < most ? tiles : most);
+    if constexpr (BWD)
+        return launch_pdl(expert_combine_bwd_kernel<T, KM>, dim3(grid), dim3(32 * kRowWarps), 0, st, a, r);
+    else
+        return launch_pdl(expert_combine_kernel<T, KM>, dim3(grid), dim3(32 * kRowWarps), 0, st, a, r);
 }
 
 template <typename T, bool BWD>
 cudaError_t run_combine(const CombineArgs &a, cudaStream_t st)
 {
     if (a.tokens <= 0) return cudaSuccess;
-    const int wpr = warps_per_row((a.width + 15) / 16);      // 512 elements per warp and turn
-    const int per = kRowWarps / wpr;
-    const unsigned grid = (unsigned)((a.tokens + per - 1) / per);
-    const bool vec = a.width % 8 == 0;
-    if constexpr (BWD) {
-        return vec ? run_combine_bwd<T, true>(a, grid, wpr, st)
-                   : run_combine_bwd<T, false>(a, grid, wpr, st);
-    } else {
-        if (vec) expert_combine_kernel<T, true><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr);
-        else expert_combine_kernel<T, false><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr);
-        return cudaGetLastError();
+    if (a.width % 8 != 0) {
+        const int wpr = warps_per_row((a.width + 7) / 8, 4);
+        const int64_t per = kRowWarps / wpr;
+        return launch_pdl(BWD ? expert_combine_bwd_shifted_kernel<T> : expert_combine_shifted_kernel<T>,
+                          dim3((unsigned)((a.tokens + per - 1) / per)), dim3(32 * kRowWarps), 0, st, a,
+                          wpr);
     }
+    RowLanes r;
+    r.lanes = 32;
+    r.wpr = 1;
+    if (a.width <= 128) {
+        r.lanes = 1;
+        while (r.lanes * 8 < a.width) r.lanes *= 2;
+    } else {
+        // a warp takes 4 turns of 256 elements, or one where that leaves SMs without a token
+        // (64 tokens of 1024: 4.4 us against 3.1)
+        r.wpr = warps_per_row((a.width + 7) / 8, 4);
+        if (a.tokens * r.wpr <= (int64_t)num_sms() * kRowWarps) r.wpr = warps_per_row((a.width + 7) / 8, 1);
+    }
+    const int64_t per = (int64_t)kRowWarps / r.wpr * (32 / r.lanes);
+    const int64_t tiles = (a.tokens + per - 1) / per;
+    if (a.choices <= 1) return run_combine_km<T, 1, BWD>(a, tiles, r, st);
+    if (a.choices <= 2) return run_combine_km<T, 2, BWD>(a, tiles, r, st);
+    if (a.choices <= 4) return run_combine_km<T, 4, BWD>(a, tiles, r, st);
+    if (a.choices <= 8) return run_combine_km<T, 8, BWD>(a, tiles, r, st);
+    return run_combine_km<T, 16, BWD>(a, tiles, r, st);
 }
 
 }  // namespace
@@ -395,7 +716,7 @@ cudaError_t run_combine(const CombineArgs &a, cudaStream_t st)
 int sort_blocks(int64_t n)
 {
     if (n <= kSortOneBlock) return 1;
-    const int64_t b = (n + 2047) / 2048;
+    const int64_t b = (n + 1023) / 1024;
     return (int)(b < kSortMaxBlocks ? b : kSortMaxBlocks);
 }
 
@@ -407,19 +728,12 @@ cudaError_t launch_expert_sort(const SortArgs &a, bool ids64, cudaStream_t st)
 cudaError_t launch_expert_dispatch(const DispatchArgs &a, cudaStream_t st)
 {
     if (a.tokens <= 0) return cudaSuccess;
-    const int64_t rb = a.row_bytes;
-    const int unit = rb % 16 == 0 ? 16 : rb % 8 == 0 ? 8 : rb % 4 == 0 ? 4 : rb % 2 == 0 ? 2 : 1;
-    const int wpr = warps_per_row((rb + unit - 1) / unit);
-    const int per = kRowWarps / wpr;
-    const unsigned grid = (unsigned)((a.tokens + per - 1) / per);
-    switch (unit) {
-    case 16: expert_dispatch_kernel<uint4><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr); break;
-    case 8: expert_dispatch_kernel<uint2><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr); break;
-    case 4: expert_dispatch_kernel<uint32_t><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr); break;
-    case 2: expert_dispatch_kernel<uint16_t><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr); break;
-    default: expert_dispatch_kernel<uint8_t><<<grid, 32 * kRowWarps, 0, st>>>(a, wpr); break;
+    switch (a.row_bytes & 15) {
+    case 0: return run_dispatch<uint4>(a, st);
+    case 8: return run_dispatch<uint2>(a, st);
+    case 4: case 12: return run_dispatch<uint32_t>(a, st);
+    default: return a.row_bytes % 2 == 0 ? run_dispatch<uint16_t>(a, st) : run_dispatch<uint8_t>(a, st);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_expert_combine(const CombineArgs &a, bool f32, cudaStream_t st)

@@ -33,12 +33,15 @@ using sm100::mbar_try_wait;
 using sm100::named_bar_sync;
 using sm100::smem_u32;
 
-constexpr int NC = 2;                   // chunks of 8 elements per thread
 constexpr int kMaxRing = 4;
 constexpr float kE4m3Max = 448.f;
 
-// How rows are read: through the ring, directly in 16-byte pieces, or element by element.
-enum Access { RING, DIRECT, ELEMENTS };
+// How rows are read: through the ring, directly, or directly where they start anywhere.
+enum Access { RING, DIRECT, SHIFTED };
+
+// Chunks of 8 elements per thread.  Rows that start anywhere need up to 7 elements more.
+template <int W, Access A>
+constexpr int chunks() { return A == SHIFTED && W == 32 ? 3 : 2; }
 
 template <int W> struct NormShape {
     static constexpr int kGroups = W < 8 ? 8 / W : 1;      // per block
@@ -46,6 +49,8 @@ template <int W> struct NormShape {
     // blocks that share an SM: the forward at 64 registers a thread, the backward at 128
     static constexpr int kFwdBlocks = 1024 / kThreads;
     static constexpr int kBwdBlocks = kThreads >= 512 ? 1 : 512 / kThreads;
+    // (the forward of rows that start anywhere: their cuts, and e4m3's, take registers)
+    static constexpr int shifted_blocks(bool e4m3) { return e4m3 ? kBwdBlocks * 3 / 2 : kFwdBlocks; }
 };
 
 // The largest magnitude that a group's scale maps to 448: its own, kept away from where
@@ -147,82 +152,88 @@ __device__ __forceinline__ Ring ring_of(uint8_t *smem, int depth, int stage_byte
 template <bool VEC>
 __device__ __forceinline__ void store8_e4m3(uint8_t *row, int c0, int width, const float (&f)[8])
 {
+    uint32_t u[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * e], f[4 * e + 1]),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * e + 2], f[4 * e + 3]),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        u[e] = lo | hi << 16;
+    }
     if constexpr (VEC) {
-        const int i = elem8<true>(c0, 0);
-        if (i >= width) return;
-        uint32_t u[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * e], f[4 * e + 1]),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * e + 2], f[4 * e + 3]),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            u[e] = lo | hi << 16;
-        }
-        *reinterpret_cast<uint2 *>(row + i) = make_uint2(u[0], u[1]);
+        if (elem8(c0) < width) *reinterpret_cast<uint2 *>(row + elem8(c0)) = make_uint2(u[0], u[1]);
     } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = elem8<false>(c0, e);
-            if (i < width) row[i] = __nv_cvt_float_to_fp8(f[e], __NV_SATFINITE, __NV_E4M3);
-        }
+        store_words<2, 1>(row + c0, row, row + width, u);
     }
 }
 
 // y * (448 / max) and the scales of one chunk of 256 columns from c0, in groups of `group`
-// columns (32, 64 or 128).  VEC: a group is group / 8 neighbouring lanes.  Otherwise it is
-// group / 32 elements of every lane.
-template <bool VEC>
+// columns (32, 64 or 128): group / 8 neighbouring lanes.
 __device__ __forceinline__ void scale_groups(float (&h)[8], int c0, int width, int group,
                                              float *scales)
 {
-    const int lane = threadIdx.x & 31;
-    if constexpr (VEC) {
-        float m = 0.f;
+    float m = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[e]));
-        for (int o = group / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-        m = scale_top(m);
-        const int i = elem8<true>(c0, 0);
-        const int shift = 31 - __clz(group);           // a power of two
-        if (i < width && (i & (group - 1)) == 0) scales[i >> shift] = m * (1.f / kE4m3Max);
-        const float back = scale_back(m);
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[e]));
+    for (int o = group / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+    m = scale_top(m);
+    const int i = elem8(c0), shift = 31 - __clz(group);    // a power of two
+    if (i < width && (i & (group - 1)) == 0) scales[i >> shift] = m * (1.f / kE4m3Max);
+    const float back = scale_back(m);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] *= back;
-    } else {
-        const int per = group / 32;                    // 1, 2 or 4 elements
-        float m[8];
+    for (int e = 0; e < 8; ++e) h[e] *= back;
+}
+
+// The same for a row that starts anywhere, all its chunks: a lane's elements may lie in two
+// neighbouring groups, so the groups' maxima meet in shared memory (`gm`, one word per group;
+// the order of maxima does not matter).
+template <int W, int NC>
+__device__ __forceinline__ void scale_groups_shifted(float (&h)[NC][8], int skew, int width, int group,
+                                                     float *scales, uint32_t *gm)
+{
+    const int t = threadIdx.x % (32 * W), wg = (threadIdx.x / 32) % W;
+    const int shift = 31 - __clz(group), groups = (width + group - 1) / group;
+    for (int g = t; g < groups; g += 32 * W) gm[g] = 0u;
+    group_sync<W>();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = fabsf(h[e]);
-        if (per > 1) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) m[e] = m[e + 1] = fmaxf(m[e], m[e + 1]);
-        }
-        if (per > 2) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) m[e] = m[e + 1] = m[e + 2] = m[e + 3] = fmaxf(m[e], m[e + 2]);
-        }
+    for (int c = 0; c < NC; ++c) {
+        const int i = elem8((c * W + wg) * 256 - skew);
+        const int lo = max(i, 0) >> shift, next = (lo + 1) << shift;
+        float m0 = 0.f, m1 = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (e % per == 0) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(kFullMask, m[e], o));
-                m[e] = scale_top(m[e]);
-                const int i = c0 + 32 * e;
-                if (lane == 0 && i < width) scales[i / group] = m[e] * (1.f / kE4m3Max);
-            } else {
-                m[e] = m[e - 1];
-            }
-            h[e] *= scale_back(m[e]);
+            if (i + e < next) m0 = fmaxf(m0, fabsf(h[c][e]));
+            else m1 = fmaxf(m1, fabsf(h[c][e]));
+        }
+        if (i + 8 > 0 && i < width) {
+            atomicMax(&gm[lo], __float_as_uint(m0));
+            if (i + 8 > next && next < width) atomicMax(&gm[lo + 1], __float_as_uint(m1));
         }
     }
+    group_sync<W>();
+    for (int g = t; g < groups; g += 32 * W)
+        scales[g] = scale_top(__uint_as_float(gm[g])) * (1.f / kE4m3Max);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int i = elem8((c * W + wg) * 256 - skew);
+        const int lo = min(max(i, 0) >> shift, groups - 1), next = (lo + 1) << shift;
+        const float b0 = scale_back(scale_top(__uint_as_float(gm[lo])));
+        const float b1 = scale_back(scale_top(__uint_as_float(gm[min(lo + 1, groups - 1)])));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[c][e] *= i + e < next ? b0 : b1;
+    }
+    group_sync<W>();
 }
 
 template <typename T, int W, bool E4M3, Access A>
-__global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBlocks)
+__global__ void __launch_bounds__(NormShape<W>::kThreads,
+                                  A == SHIFTED ? NormShape<W>::shifted_blocks(E4M3)
+                                               : NormShape<W>::kFwdBlocks)
     rms_norm_kernel(const __grid_constant__ RmsArgs a, int depth)
 {
-    constexpr bool VEC = A != ELEMENTS;
+    constexpr bool VEC = A != SHIFTED;
+    constexpr int NC = chunks<W, A>();
     constexpr int kGroups = NormShape<W>::kGroups;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float buf[2][NormShape<W>::kThreads / 32];
@@ -231,6 +242,8 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBloc
     const int64_t stride = (int64_t)gridDim.x * kGroups;
     int64_t row = (int64_t)blockIdx.x * kGroups + group;
     const int width = a.width;
+    // the same for all rows of a group: the stride is a multiple of 8 (or there is one row)
+    const int skew = lead_of<VEC>(row, width);
     const uint32_t row_bytes = (uint32_t)width * sizeof(T);
     const uint8_t *const in[2] = {reinterpret_cast<const uint8_t *>(a.x),
                                   reinterpret_cast<const uint8_t *>(a.resid)};
@@ -252,12 +265,14 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBloc
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         if (a.weight) {
-            load8<VEC>(a.weight, (c * W + wg) * 256, width, w[c]);
+            load8<VEC>(a.weight, (c * W + wg) * 256 - skew, width, a.weight, a.weight + width, w[c]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[c][e] = 1.f;
         }
     }
+    const T *x_begin = reinterpret_cast<const T *>(a.x), *x_end = x_begin + a.rows * width;
+    const T *r_begin = reinterpret_cast<const T *>(a.resid), *r_end = r_begin + a.rows * width;
     int stage = 0;
     uint32_t parity = 0;
     for (; row < a.rows; row += stride) {
@@ -273,11 +288,11 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBloc
         float h[NC][8];
         float ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load8<VEC>(x, (c * W + wg) * 256, width, h[c]);
+        for (int c = 0; c < NC; ++c) load8<VEC>(x, (c * W + wg) * 256 - skew, width, x_begin, x_end, h[c]);
         if (r) {
             float b[NC][8];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) load8<VEC>(r, (c * W + wg) * 256, width, b[c]);
+            for (int c = 0; c < NC; ++c) load8<VEC>(r, (c * W + wg) * 256 - skew, width, r_begin, r_end, b[c]);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBloc
         if (a.sum) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                store8<VEC>(reinterpret_cast<T *>(a.sum) + base, (c * W + wg) * 256, width, h[c]);
+                store8<VEC>(reinterpret_cast<T *>(a.sum) + base, (c * W + wg) * 256 - skew, width, h[c]);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -312,7 +327,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBloc
         if constexpr (!E4M3) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                store8<VEC>(reinterpret_cast<T *>(a.y) + base, (c * W + wg) * 256, width, h[c]);
+                store8<VEC>(reinterpret_cast<T *>(a.y) + base, (c * W + wg) * 256 - skew, width, h[c]);
             if constexpr (W > 1) group_sync<W>();          // buf is used again
         } else {
             if (a.group == 0) {
@@ -328,16 +343,20 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kFwdBloc
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) h[c][e] *= back;
+            } else if constexpr (!VEC) {
+                const int groups = (width + a.group - 1) / a.group;
+                scale_groups_shifted<W, NC>(h, skew, width, a.group, a.scales + row * groups,
+                                            reinterpret_cast<uint32_t *>(smem) + group * groups);
             } else {
                 const int groups = (width + a.group - 1) / a.group;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    scale_groups<VEC>(h[c], (c * W + wg) * 256, width, a.group, a.scales + row * groups);
+                    scale_groups(h[c], (c * W + wg) * 256, width, a.group, a.scales + row * groups);
                 if constexpr (W > 1) group_sync<W>();
             }
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                store8_e4m3<VEC>(reinterpret_cast<uint8_t *>(a.y) + base, (c * W + wg) * 256, width, h[c]);
+                store8_e4m3<VEC>(reinterpret_cast<uint8_t *>(a.y) + base, (c * W + wg) * 256 - skew, width, h[c]);
         }
     }
 }
@@ -349,7 +368,8 @@ template <typename T, int W, Access A>
 __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBlocks)
     rms_norm_bwd_kernel(const __grid_constant__ RmsBwdArgs a, int depth)
 {
-    constexpr bool VEC = A != ELEMENTS;
+    constexpr bool VEC = A != SHIFTED;
+    constexpr int NC = chunks<W, A>();
     constexpr int kGroups = NormShape<W>::kGroups;
     extern __shared__ __align__(128) uint8_t smem[];       // the ring, then [kGroups][width] floats
     __shared__ float buf[2][NormShape<W>::kThreads / 32];
@@ -358,6 +378,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
     const int64_t stride = (int64_t)gridDim.x * kGroups;
     int64_t row = (int64_t)blockIdx.x * kGroups + group;
     const int width = a.width;
+    const int skew = lead_of<VEC>(row, width);             // of all rows of the group
     const uint32_t row_bytes = (uint32_t)width * sizeof(T);
     const uint8_t *const in[3] = {reinterpret_cast<const uint8_t *>(a.dy),
                                   reinterpret_cast<const uint8_t *>(a.h),
@@ -381,13 +402,16 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
     float acc[NC][8], w[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        if (a.weight) load8<VEC>(a.weight, (c * W + wg) * 256, width, w[c]);
+        if (a.weight) load8<VEC>(a.weight, (c * W + wg) * 256 - skew, width, a.weight, a.weight + width, w[c]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             acc[c][e] = 0.f;
             if (!a.weight) w[c][e] = 1.f;
         }
     }
+    const T *dy_begin = reinterpret_cast<const T *>(a.dy), *dy_end = dy_begin + a.rows * width;
+    const T *h_begin = reinterpret_cast<const T *>(a.h), *h_end = h_begin + a.rows * width;
+    const T *ds_begin = reinterpret_cast<const T *>(a.dsum), *ds_end = ds_begin + a.rows * width;
     int stage = 0, flip = 0;
     uint32_t parity = 0;
     float rs_next = row < a.rows ? a.rstd[row] : 0.f;      // one row ahead
@@ -408,8 +432,8 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            load8<VEC>(dy, (c * W + wg) * 256, width, g[c]);
-            load8<VEC>(hp, (c * W + wg) * 256, width, h[c]);
+            load8<VEC>(dy, (c * W + wg) * 256 - skew, width, dy_begin, dy_end, g[c]);
+            load8<VEC>(hp, (c * W + wg) * 256 - skew, width, h_begin, h_end, h[c]);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -425,13 +449,13 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float o[8];
-            if (ds) load8<VEC>(ds, (c * W + wg) * 256, width, o);
+            if (ds) load8<VEC>(ds, (c * W + wg) * 256 - skew, width, ds_begin, ds_end, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float d = rs * (g[c][e] - h[c][e] * dot);
                 o[e] = ds ? d + o[e] : d;
             }
-            store8<VEC>(dx, (c * W + wg) * 256, width, o);
+            store8<VEC>(dx, (c * W + wg) * 256 - skew, width, o);
         }
         if constexpr (A == RING) {
             group_sync<W>();                               // the group has read the stage
@@ -446,15 +470,29 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
     if (!a.dweight) return;
     float *part = a.part + (int64_t)blockIdx.x * width;
     if constexpr (kGroups == 1) {
+        // (the parts' own rows start on 16 bytes where VEC)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) store8<VEC>(part, (c * W + wg) * 256, width, acc[c]);
+        for (int c = 0; c < NC; ++c) {
+            const int i = elem8((c * W + wg) * 256 - skew);
+            if constexpr (VEC) {
+                store8<true>(part, (c * W + wg) * 256, width, acc[c]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (i + e >= 0 && i + e < width) part[i + e] = acc[c][e];
+            }
+        }
     } else {
         // the groups' stages are done with: their memory holds the groups' parts
         float *dws = reinterpret_cast<float *>(smem);
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            store8<VEC>(dws + group * width, (c * W + wg) * 256, width, acc[c]);
+        for (int c = 0; c < NC; ++c) {
+            const int i = elem8((c * W + wg) * 256 - skew);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e >= 0 && i + e < width) dws[group * width + i + e] = acc[c][e];
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < width; i += blockDim.x) {
             float s = 0.f;
@@ -487,11 +525,12 @@ __global__ void __launch_bounds__(1024) rms_dweight_kernel(const float *__restri
     if (lane == 0 && blockIdx.x * 32 + strand < width) dweight[blockIdx.x * 32 + strand] = r;
 }
 
-// Warps per row: 512 columns per warp.
+// Warps per row: 512 columns per warp, with room for the lead of rows that start anywhere.
 int warps_for(int width)
 {
+    const int room = width % 8 ? width + 7 : width;
     int w = 1;
-    while (w < 32 && w * 512 < width) w *= 2;
+    while (w < 32 && w * 512 < room) w *= 2;
     return w;
 }
 
@@ -534,8 +573,13 @@ cudaError_t run_fwd(const RmsArgs &a, cudaStream_t st)
     using S = NormShape<W>;
     const int64_t most = (int64_t)num_sms() * S::kFwdBlocks;
     const int64_t blocks = (a.rows + S::kGroups - 1) / S::kGroups;
-    if (a.width % 8 != 0)
-        return launch_norm(rms_norm_kernel<T, W, E4M3, ELEMENTS>, a, blocks, S::kThreads, 0, 0, st);
+    if (a.width % 8 != 0) {
+        // groups keep their rows' alignment: a stride of a multiple of 8 rows
+        const int64_t stay = (int64_t)num_sms() * S::shifted_blocks(E4M3) / 8 * 8;
+        const size_t maxima = E4M3 && a.group ? (size_t)S::kGroups * ((a.width + a.group - 1) / a.group) * 4 : 0;
+        return launch_norm(rms_norm_kernel<T, W, E4M3, SHIFTED>, a, std::min(blocks, stay),
+                           S::kThreads, maxima, 0, st);
+    }
     if (blocks <= most)
         return launch_norm(rms_norm_kernel<T, W, E4M3, DIRECT>, a, blocks, S::kThreads, 0, 0, st);
     const int64_t stage = (int64_t)a.width * sizeof(T) * (a.resid ? 2 : 1);
@@ -565,7 +609,7 @@ cudaError_t run_bwd(const RmsBwdArgs &a, cudaStream_t st)
     const size_t parts = S::kGroups > 1 && a.dweight ? (size_t)S::kGroups * a.width * 4 : 0;
     cudaError_t e;
     if (a.width % 8 != 0) {
-        e = launch_norm(rms_norm_bwd_kernel<T, W, ELEMENTS>, a, blocks, S::kThreads, parts, 0, st);
+        e = launch_norm(rms_norm_bwd_kernel<T, W, SHIFTED>, a, blocks, S::kThreads, parts, 0, st);
     } else if (a.rows <= (int64_t)blocks * S::kGroups) {
         e = launch_norm(rms_norm_bwd_kernel<T, W, DIRECT>, a, blocks, S::kThreads, parts, 0, st);
     } else {
@@ -597,7 +641,9 @@ int rms_bwd_blocks(int64_t rows, int width)
 {
     // 512 threads per SM; more blocks would only add rows of partial sums
     const int w = warps_for(width), per = w < 8 ? 8 / w : 1;
-    const int64_t need = (rows + per - 1) / per, most = w >= 16 ? 148 : 296;
+    const int64_t need = (rows + per - 1) / per;
+    // (rows that start anywhere keep their alignment with a stride of a multiple of 8)
+    const int64_t most = w < 16 ? 296 : width % 8 ? 144 : 148;
     return (int)std::max<int64_t>(1, std::min<int64_t>(need, most));
 }
 
