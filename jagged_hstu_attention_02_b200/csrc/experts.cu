@@ -445,17 +445,17 @@ struct Places {
 __device__ __forceinline__ int lane_c0(int c0, int lane) { return c0 + 8 * (lane - (int)(threadIdx.x & 31)); }
 
 // Blocks per SM, so that the pieces of 4 choices fit the registers (fp32 takes twice as many).
-template <typename T, int KM>
+template <typename T, int KM, bool BWD>
 constexpr int combine_blocks()
 {
-    return sizeof(T) == 2 ? (KM <= 4 ? 4 : KM <= 8 ? 3 : 2) : KM <= 4 ? 3 : 2;
+    return sizeof(T) == 2 ? (KM <= 4 && !BWD ? 4 : KM <= 8 ? 3 : 2) : KM <= 4 ? 3 : 2;
 }
 
 // KM: the choices, rounded up to a power of two.  Blocks stay and walk the tokens; the places
 // and weights of the next token are fetched while this one's rows move, and the rows of 4
 // choices before the first of them is used.
 template <typename T, int KM>
-__global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM>())
+__global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM, false>())
     expert_combine_kernel(const __grid_constant__ CombineArgs a, const RowLanes r)
 {
     constexpr int KB = KM < 4 ? KM : 4;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM>())
 }
 
 template <typename T, int KM>
-__global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM>())
+__global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM, true>())
     expert_combine_bwd_kernel(const __grid_constant__ CombineArgs a, const RowLanes r)
 {
     constexpr int KB = KM < 4 ? KM : 4;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 5)
 template <typename T, int KM, bool BWD>
 cudaError_t run_combine_km(const CombineArgs &a, int64_t tiles, const RowLanes &r, cudaStream_t st)
 {
-    const int64_t most = (int64_t)num_sms() * combine_blocks<T, KM>();
+    const int64_t most = (int64_t)num_sms() * combine_blocks<T, KM, BWD>();
     const unsigned grid = (unsigned)(tiles < most ? tiles : most);
     if constexpr (BWD)
         return launch_pdl(expert_combine_bwd_kernel<T, KM>, dim3(grid), dim3(32 * kRowWarps), 0, st, a, r);
@@ -697,9 +697,9 @@ cudaError_t run_combine(const CombineArgs &a, cudaStream_t st)
         r.lanes = 1;
         while (r.lanes * 8 < a.width) r.lanes *= 2;
     } else {
-        // a warp takes 4 turns of 256 elements, or one where that leaves SMs without a token
-        // (64 tokens of 1024: 4.4 us against 3.1)
-        r.wpr = warps_per_row((a.width + 7) / 8, 4);
+        // a warp takes 4 turns of 512 bytes (2 of 1024), or one where that leaves SMs without a
+        // token (64 tokens of 1024 bf16: 4.4 us against 3.1)
+        r.wpr = warps_per_row((a.width + 7) / 8, sizeof(T) == 2 ? 4 : 2);
         if (a.tokens * r.wpr <= (int64_t)num_sms() * kRowWarps) r.wpr = warps_per_row((a.width + 7) / 8, 1);
     }
     const int64_t per = (int64_t)kRowWarps / r.wpr * (32 / r.lanes);
