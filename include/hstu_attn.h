@@ -427,7 +427,9 @@ hstu_status_t hstu_expert_combine_bwd(const void *dout, const void *y, const int
  * hstu_expert_proj_bwd: the gradients of hstu_expert_proj's product.  dx [rows, d_in] = dout w[e]^T
  * (NULL: not computed); with silu_pre [rows, d_in] (NULL for none) times SiLU'(silu_pre), the
  * gradient ahead of the SiLU that made x.  dw [num_experts, d_in, d_out] = sum over the expert's
- * rows of x_s^T dout_s (NULL: not computed; zeros for an expert without rows).  bf16.
+ * rows of x_s^T dout_s (NULL: not computed; zeros for an expert without rows).  bf16.  dw needs a
+ * workspace of hstu_expert_proj_bwd_workspace_size bytes (often 0: sums of parts of the rows, where
+ * few and small matrices meet many rows).
  * Device pointers 16-byte aligned; each call enqueues kernels on `stream` and allocates nothing.
  */
 hstu_status_t hstu_expert_proj(const void *x, const void *w, const int64_t *offsets, int64_t rows,
@@ -440,7 +442,10 @@ hstu_status_t hstu_expert_proj_e4m3(const void *x, const float *x_scales, const 
 hstu_status_t hstu_expert_proj_bwd(const void *dout, const void *x, const void *w,
                                    const int64_t *offsets, const void *silu_pre, int64_t rows,
                                    int32_t num_experts, int32_t d_in, int32_t d_out, void *dx,
-                                   void *dw, int32_t *status, void *stream);
+                                   void *dw, int32_t *status, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+hstu_status_t hstu_expert_proj_bwd_workspace_size(int64_t rows, int32_t num_experts, int32_t d_in,
+                                                  int32_t d_out, size_t *bytes);
 
 /* Static description of a status code. */
 const char *hstu_status_string(hstu_status_t status);

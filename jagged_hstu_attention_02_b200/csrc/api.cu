@@ -749,20 +749,35 @@ hstu_status_t hstu_expert_proj_e4m3(const void *x, const float *x_scales, const 
     return HSTU_OK;
 }
 
+hstu_status_t hstu_expert_proj_bwd_workspace_size(int64_t rows, int32_t num_experts, int32_t d_in,
+                                                  int32_t d_out, size_t *bytes)
+{
+    if (!bytes || !proj_shape_ok(rows, num_experts, d_in, d_out, 8)) return HSTU_ERR_INVALID_ARGUMENT;
+    const int slices = expert_dw_slices(rows, num_experts, d_in, d_out);
+    *bytes = slices > 1 ? (size_t)slices * num_experts * d_in * d_out * 4 : 0;
+    return HSTU_OK;
+}
+
 hstu_status_t hstu_expert_proj_bwd(const void *dout, const void *x, const void *w,
                                    const int64_t *offsets, const void *silu_pre, int64_t rows,
                                    int32_t num_experts, int32_t d_in, int32_t d_out, void *dx,
-                                   void *dw, int32_t *status, void *stream)
+                                   void *dw, int32_t *status, void *workspace,
+                                   size_t workspace_bytes, void *stream)
 {
     if (!proj_shape_ok(rows, num_experts, d_in, d_out, 8)) return HSTU_ERR_INVALID_ARGUMENT;
     if (!offsets || (rows > 0 && (!dout || (dx && !w) || (dw && !x))) ||
-        !all_aligned16({dout, x, w, offsets, silu_pre, dx, dw}))
+        !all_aligned16({dout, x, w, offsets, silu_pre, dx, dw, workspace}))
         return HSTU_ERR_INVALID_ARGUMENT;
+    size_t need = 0;
+    if (dw) hstu_expert_proj_bwd_workspace_size(rows, num_experts, d_in, d_out, &need);
+    if (need > 0 && !workspace) return HSTU_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return HSTU_ERR_WORKSPACE_TOO_SMALL;
     ProjArgs a = proj_args(x, w, offsets, rows, num_experts, d_in, d_out, status);
     a.dout = dout;
     a.silu_pre = silu_pre;
     a.dx = dx;
     a.dw = dw;
+    a.partial = reinterpret_cast<float *>(workspace);
     if (dx) HSTU_CUDA_TRY(launch_expert_proj_dx(a, reinterpret_cast<cudaStream_t>(stream)));
     if (dw) HSTU_CUDA_TRY(launch_expert_proj_dw(a, reinterpret_cast<cudaStream_t>(stream)));
     return HSTU_OK;

@@ -35,9 +35,11 @@ enum Product { P_FWD = 0, P_E4M3 = 1, P_DX = 2, P_DW = 3 };
 constexpr int EBM = 128;             // rows of a CTA's output tile (TMEM lanes)
 constexpr int EBN = 128;             // columns of the second operand that a CTA stages
 constexpr int kSlice = 128;          // bytes of the contraction per stage and row
-constexpr int kStages = 5;
+constexpr int kMaxStages = 6;
 constexpr int kSmallBox = 16;        // rows of the small A box, for tiles with few rows
 constexpr int kEpiWarps = 16;
+constexpr int kBand = 8;             // column tiles that the tiles in flight share
+constexpr int kMaxSorted = 256;      // experts that P_DW puts in order of their rows
 constexpr int kEThreads = 32 * (2 + kEpiWarps);
 
 struct EGemmArgs {
@@ -48,6 +50,9 @@ struct EGemmArgs {
     int kc;                          // contraction length (P_DW: the expert's rows instead)
     int m, n;                        // P_DW: rows of an output tile's matrix; output columns
     int silu;
+    int stages;                      // of the ring
+    int slices;                      // P_DW: parts that an expert's rows are cut into
+    float *partial;                  // P_DW with slices > 1: their sums [slices, experts, m, n]
     const float *x_scales, *w_scales;
     const __nv_bfloat16 *silu_pre;   // P_DX
     __nv_bfloat16 *out, *pre;
@@ -57,15 +62,27 @@ struct EGemmArgs {
 };
 
 // Shared memory of a CTA.  CG CTAs work on one tile of CG * 128 rows x CG * 128 columns: each
-// stages 128 rows of A and 128 columns of B, 32 KB per stage.
+// stages 128 rows of A and 128 columns of B, 16 KB each per slice of the contraction, in as many
+// stages as there is room for (4 to 6, by the size of the experts' table).
+constexpr int AB = EBM * kSlice, BB = EBN * kSlice;
+
+template <int CG>
 struct ELayout {
-    static constexpr int AB = EBM * kSlice;           // 16 KB
-    static constexpr int BB = EBN * kSlice;           // 16 KB
-    static constexpr int A_OFF = 0;
-    static constexpr int B_OFF = kStages * AB;
-    static constexpr int C_OFF = B_OFF + kStages * BB;      // 2 KB per epilogue warp
-    static constexpr int BAR_OFF = C_OFF + kEpiWarps * 2048;
-    static constexpr int TAB_OFF = BAR_OFF + 512;     // tile prefix and row starts
+    static constexpr int kWarpStage = CG * 2048;      // of an epilogue warp: 32 rows x 32 CG columns
+    static constexpr int kBarBytes = 512;
+    // [A stages][B stages][epilogue][barriers][table]
+    static __host__ __device__ int c_off(int stages) { return stages * (AB + BB); }
+    static __host__ __device__ int bar_off(int stages) { return c_off(stages) + kEpiWarps * kWarpStage; }
+    static __host__ int bytes(int stages, int experts)
+    {
+        return bar_off(stages) + kBarBytes + (3 * experts + 1) * 4 + 1024 /* alignment */;
+    }
+    static __host__ int stages(int experts)
+    {
+        int n = kMaxStages;
+        while (bytes(n, experts) > 232448) --n;
+        return n;
+    }
 };
 
 // TMA loads into this CTA's shared memory.  CG = 2: `bar` is an address in the pair's shared
@@ -250,18 +267,41 @@ __device__ __forceinline__ void egemm_flag(const EGemmArgs &a, int bits)
 }
 
 // The experts' rows and row tiles, in shared memory: expert e's rows are [row0[e], row0[e] +
-// cnt[e]) and its row tiles [tile0[e], tile0[e + 1]).
+// cnt[e]) and its row tiles [tile0[e], tile0[e + 1]).  P_DW, whose tiles cost what their expert
+// has rows: tile0 lists the experts, those with the most rows first.
 struct ExpertTable {
     int32_t *tile0, *row0, *cnt;
 };
 
 // Fills the table (all threads of the block).  An expert whose offsets are invalid has no rows.
-template <int CG>
+template <int P, int CG>
 __device__ __forceinline__ void fill_table(const EGemmArgs &a, const ExpertTable &t, int32_t *wsum)
 {
     constexpr int kRows = CG * EBM;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kEThreads / 32;
+    if constexpr (P == P_DW) {
+        for (int e = tid; e < a.experts; e += kEThreads) {
+            int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
+            if (lo < 0 || hi < lo || hi > a.rows) {
+                if (blockIdx.x == 0) egemm_flag(a, HSTU_DEV_BAD_OFFSETS);
+                lo = hi = 0;
+            }
+            t.row0[e] = (int)lo;
+            t.cnt[e] = (int)(hi - lo);
+        }
+        __syncthreads();
+        for (int e = tid; e < a.experts; e += kEThreads) {
+            int rank = e;
+            if (a.experts <= kMaxSorted) {
+                const int mine = t.cnt[e];
+                rank = 0;
+                for (int o = 0; o < a.experts; ++o) rank += t.cnt[o] > mine || (t.cnt[o] == mine && o < e);
+            }
+            t.tile0[rank] = e;
+        }
+        return;
+    }
     int base = 0;
     for (int e0 = 0; e0 < a.experts; e0 += kEThreads) {
         const int e = e0 + tid;
@@ -302,8 +342,8 @@ template <int P>
 __device__ __forceinline__ uint32_t stage_bytes(int rows)
 {
     const bool small = P != P_DW && rows <= 64;
-    return ELayout::BB + (small ? (rows + kSmallBox - 1) / kSmallBox * kSmallBox * kSlice
-                                : (uint32_t)ELayout::AB);
+    return BB + (small ? (rows + kSmallBox - 1) / kSmallBox * kSmallBox * kSlice
+                                : (uint32_t)AB);
 }
 
 struct ETile {
@@ -311,54 +351,97 @@ struct ETile {
     int m0, rows;     // first row (of the sorted rows; P_DW: of the matrix) and rows to store
     int n0;           // first output column
     int kbeg, kcnt;   // contraction: first index and length
+    int slice;        // P_DW: of the expert's rows
 };
 
 template <int P, int CG>
 __device__ __forceinline__ int tile_count(const EGemmArgs &a, const ExpertTable &t)
 {
     const int nt = (a.n + CG * EBN - 1) / (CG * EBN);
-    return P == P_DW ? a.experts * ((a.m + CG * EBM - 1) / (CG * EBM)) * nt
+    return P == P_DW ? a.slices * a.experts * ((a.m + CG * EBM - 1) / (CG * EBM)) * nt
                      : t.tile0[a.experts] * nt;
 }
 
+// The tile that CTA (pair) `first` of `stride` takes in its turn w, or -1 after its last.
+// P_DW deals back and forth, so that whoever takes the longest tile of one turn takes the
+// shortest of the next.
+template <int P>
+__device__ __forceinline__ int deal(int w, int first, int stride, int ntiles)
+{
+    const int tile = w * stride + (P == P_DW && (w & 1) ? stride - 1 - first : first);
+    return tile < ntiles ? tile : -1;
+}
+
+// An expert's tiles are numbered along bands of kBand column tiles, rows first: the tiles that
+// run at the same time then cover about as many rows as columns of the product, and share their
+// operands in L2 (8192 x 8192 x 8192 bf16 with whole rows of tiles: 765 us).
 template <int P, int CG>
 __device__ __forceinline__ ETile tile_of(const EGemmArgs &a, const ExpertTable &t, int tile)
 {
     constexpr int kRows = CG * EBM;
     const int nt = (a.n + CG * EBN - 1) / (CG * EBN);
     ETile r;
-    r.n0 = (tile % nt) * (CG * EBN);
-    const int q = tile / nt;
+    int mt, i;                               // the expert's row tiles, the tile's number in it
+    r.slice = 0;
     if constexpr (P == P_DW) {
-        const int mt = (a.m + kRows - 1) / kRows;
-        r.e = q / mt;
-        r.m0 = (q % mt) * kRows;
-        r.rows = min(kRows, a.m - r.m0);
-        r.kbeg = t.row0[r.e];
-        r.kcnt = t.cnt[r.e];
+        if (a.slices > 1) {
+            r.slice = tile % a.slices;
+            tile /= a.slices;
+        }
+        mt = (a.m + kRows - 1) / kRows;
+        const int q = tile / (mt * nt);
+        r.e = t.tile0[q];
+        i = tile - q * (mt * nt);
     } else {
+        const int q = tile / nt;
         int lo = 0, hi = a.experts;          // the last expert whose first tile is <= q
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (t.tile0[mid] <= q) lo = mid; else hi = mid;
         }
         r.e = lo;
-        const int off = (q - t.tile0[lo]) * kRows;
-        r.m0 = t.row0[lo] + off;
-        r.rows = min(kRows, t.cnt[lo] - off);
+        mt = t.tile0[lo + 1] - t.tile0[lo];
+        i = tile - t.tile0[lo] * nt;
+    }
+    const int band = i / (mt * kBand), j = i - band * (mt * kBand);
+    const int cols = min(kBand, nt - band * kBand);
+    const int row = j / cols;
+    r.n0 = (band * kBand + j - row * cols) * (CG * EBN);
+    if constexpr (P == P_DW) {
+        r.m0 = row * kRows;
+        r.rows = min(kRows, a.m - r.m0);
+        r.kbeg = t.row0[r.e];
+        r.kcnt = t.cnt[r.e];
+        if (a.slices > 1) {                  // whole steps of 64 rows, as evenly as they go
+            const int steps = (r.kcnt + 63) / 64;
+            const int beg = (int)((int64_t)steps * r.slice / a.slices) * 64;
+            const int end = min(r.kcnt, (int)((int64_t)steps * (r.slice + 1) / a.slices) * 64);
+            r.kbeg += beg;
+            r.kcnt = max(0, end - beg);
+        }
+    } else {
+        r.m0 = t.row0[r.e] + row * kRows;
+        r.rows = min(kRows, t.cnt[r.e] - row * kRows);
         r.kbeg = 0;
         r.kcnt = a.kc;
     }
     return r;
 }
 
-// x * sigmoid(x) and its slope, on the hardware's exponential and reciprocal (2 ulp each).
-__device__ __forceinline__ float sigmoid_fast(float x)
+// sigmoid(x) and sigmoid(y) on the hardware's exponential and reciprocal (2 ulp each), one
+// reciprocal for both: 1 / a = b / (a b).  The special-function unit takes 8 cycles per warp and
+// call, so 4 calls for two values of a 256-wide tile would outlast its MMAs below 512 of the
+// contraction.  Exponents stop at 2^62 (x = -43), where the product would leave fp32's range:
+// from there on sigmoid is 2^-62 instead of less, an error of x SiLU(x) below 1e-17.
+__device__ __forceinline__ void sigmoid2(float x, float y, float &sx, float &sy)
 {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
+    float ex, ey, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(fminf(x * -1.4426950408889634f, 62.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(fminf(y * -1.4426950408889634f, 62.f)));
+    const float a = 1.f + ex, b = 1.f + ey;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+    sx = r * b;
+    sy = r * a;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&f)[8])
@@ -367,40 +450,39 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
                       pack_bf16x2(f[6], f[7]));
 }
 
-// 16-byte piece c of row `row` of a warp's 32 x 64 bytes, swizzled so that 8 rows' pieces c, and
-// the pieces of 2 rows, lie in different banks.
+// Piece c (16 bytes) of row `row` of a warp's 32 rows x NP pieces in shared memory, swizzled so
+// that 8 rows' pieces c, and neighbouring pieces of a row, lie in different banks.
+template <int NP>
 __device__ __forceinline__ uint4 *staged(uint8_t *stage, int row, int c)
 {
-    return reinterpret_cast<uint4 *>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
+    return reinterpret_cast<uint4 *>(
+        stage + row * (16 * NP) + ((c ^ (NP == 8 ? row & 7 : (row >> 1) & 3)) * 16));
 }
 
-// This lane's row (32 bf16) of the warp's 32 to shared memory, and from there 4 lanes a row to
-// out[(out0 + row) * n + nb ...], rows and columns that exist.
-__device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&o)[4], __nv_bfloat16 *out,
-                                           int64_t out0, int rows, int nb, int n)
+// The staged rows to out[(out0 + row) * n + nb ...], NP lanes a row, rows and columns that exist.
+template <int NP>
+__device__ __forceinline__ void store_rows(uint8_t *stage, __nv_bfloat16 *out, int64_t out0, int rows,
+                                           int nb, int n)
 {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *staged(stage, lane, i) = o[i];
-    __syncwarp();
-    const int r0 = lane / 4, col = nb + 8 * (lane & 3);
+    const int r0 = lane / NP, col = nb + 8 * (lane % NP);
     __nv_bfloat16 *at = out + (out0 + r0) * n + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint4 x = *staged(stage, 8 * i + r0, lane & 3);
-        if (8 * i + r0 < rows && col < n) *reinterpret_cast<uint4 *>(at) = x;
-        at += (int64_t)8 * n;
+    for (int i = 0; i < NP; ++i) {
+        const int row = i * (32 / NP) + r0;
+        const uint4 x = *staged<NP>(stage, row, lane % NP);
+        if (row < rows && col < n) *reinterpret_cast<uint4 *>(at) = x;
+        at += (int64_t)(32 / NP) * n;
     }
-    __syncwarp();
 }
 
 // 32 accumulator columns to bf16: scales, SiLU or the SiLU's slope applied in fp32 before the
 // one rounding.  xs, ws: the row's scale and the columns' (P_E4M3); pv: this row's silu_pre
-// (P_DX); po: the product itself (P_FWD with pre).
+// (P_DX).  product: without the SiLU.
 template <int P>
 __device__ __forceinline__ void convert32(const EGemmArgs &a, bool none, float xs, const float4 *ws,
-                                          const uint32_t (&v)[32], const uint4 (&pv)[4],
-                                          uint4 (&o)[4], uint4 (&po)[4])
+                                          const uint32_t (&v)[32], const uint4 (&pv)[4], bool product,
+                                          uint4 (&o)[4])
 {
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -419,19 +501,22 @@ __device__ __forceinline__ void convert32(const EGemmArgs &a, bool none, float x
                 for (int y = 0; y < 4; ++y) {
                     const float p0 = __uint_as_float(u4[y] << 16);
                     const float p1 = __uint_as_float(u4[y] & 0xFFFF0000u);
-                    const float s0 = sigmoid_fast(p0), s1 = sigmoid_fast(p1);
+                    float s0, s1;
+                    sigmoid2(p0, p1, s0, s1);
                     f[2 * y] *= s0 * fmaf(p0, 1.f - s0, 1.f);
                     f[2 * y + 1] *= s1 * fmaf(p1, 1.f - s1, 1.f);
                 }
             }
         }
-        if constexpr (P == P_FWD) {
-            if (a.pre) po[h] = pack8(f);
-        }
         if constexpr (P == P_FWD || P == P_E4M3) {
-            if (a.silu) {
+            if (a.silu && !product) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) f[x] *= sigmoid_fast(f[x]);
+                for (int x = 0; x < 8; x += 2) {
+                    float s0, s1;
+                    sigmoid2(f[x], f[x + 1], s0, s1);
+                    f[x] *= s0;
+                    f[x + 1] *= s1;
+                }
             }
         }
         o[h] = pack8(f);
@@ -448,29 +533,34 @@ enum EBar { E_FULL = 0, E_EMPTY = 8, E_TAIL = 16, E_READY = 24, EACC_FULL = 32, 
 template <int P, int CG>
 __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_constant__ EGemmArgs a)
 {
-    using L = ELayout;
-    constexpr int ST = kStages;
+    using L = ELayout<CG>;
+    const int ST = a.stages;
     constexpr int BN = CG * EBN;                        // columns of the pair's tile
     constexpr int KB = P == P_E4M3 ? 128 : 64;          // contraction per stage
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR_OFF);
-    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::BAR_OFF + 8 * 40);
-    int32_t *wsum = reinterpret_cast<int32_t *>(sm + L::BAR_OFF + 8 * 41);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bar_off(ST));
+    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 40);
+    int32_t *wsum = reinterpret_cast<int32_t *>(bars + 41);
     ExpertTable tab;
-    tab.tile0 = reinterpret_cast<int32_t *>(sm + L::TAB_OFF);
+    tab.tile0 = reinterpret_cast<int32_t *>(sm + L::bar_off(ST) + L::kBarBytes);
     tab.row0 = tab.tile0 + a.experts + 1;
     tab.cnt = tab.row0 + a.experts;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
     const int first = blockIdx.x / CG, stride = gridDim.x / CG;
     if (threadIdx.x == 0) {
+        prefetch_tmap(&a.ta);
+        prefetch_tmap(&a.ta_small);
+        prefetch_tmap(&a.tb);
         for (int x = 0; x < E_NBARS; ++x)
             mbar_init(&bars[x], x == EACC_EMPTY || x == EACC_EMPTY + 1 ? CG * kEpiWarps : 1);
         fence_mbar_init();
     }
     if (warp == 2) tmem_take<CG>(slot, 2 * BN);
-    fill_table<CG>(a, tab, wsum);
+    grid_dep_wait();
+    grid_dep_release();
+    fill_table<P, CG>(a, tab, wsum);
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) pair_sync();
@@ -482,11 +572,12 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
     if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------------------- TMA producer
-            prefetch_tmap(&a.ta);
-            prefetch_tmap(&a.tb);
-            int g = 0;
+            int s = 0, issued = 0;                       // stage, copies of stages so far
+            uint32_t phase = 0;                          // of the stage's next use
             bool ok = true;
-            for (int tile = first; ok && tile < ntiles; tile += stride) {
+            for (int turn = 0; ok; ++turn) {
+                const int tile = deal<P>(turn, first, stride, ntiles);
+                if (tile < 0) break;
                 const ETile r = tile_of<P, CG>(a, tab, tile);
                 const int kch = (r.kcnt + KB - 1) / KB;
                 const int m0 = r.m0 + rank * EBM, n0 = r.n0 + rank * EBN;
@@ -496,13 +587,13 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                 const uint32_t bytes = stage_bytes<P>(rows);
                 const uint32_t both = CG == 1 ? bytes : bytes + stage_bytes<P>(
                     max(0, min(EBM, r.rows - EBM)));
-                for (int kc = 0; kc < kch; ++kc, ++g) {
-                    const int s = g % ST;
-                    if (g >= ST && !mbar_wait(&bars[E_EMPTY + s], ((g / ST) - 1) & 1, a.wait_limit)) {
+                for (int kc = 0; kc < kch; ++kc) {
+                    // (the phase before the first counts as over)
+                    if (!mbar_wait(&bars[E_EMPTY + s], phase ^ 1, a.wait_limit)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *as = sm + L::A_OFF + s * L::AB, *bs = sm + L::B_OFF + s * L::BB;
+                    uint8_t *as = sm + s * AB, *bs = sm + ST * AB + s * BB;
                     const bool tail = CG == 2 && P == P_DW && r.kcnt - kc * KB < KB;
                     if (rank == 0) mbar_arrive_expect_tx(&bars[E_FULL + s], tail ? bytes : both);
                     else if (tail) mbar_arrive_expect_tx(&bars[E_TAIL + s], bytes);
@@ -529,6 +620,11 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                             load_3d<CG>(bs, &a.tb, full, kc * KB, n0, r.e);
                         }
                     }
+                    ++issued;
+                    if (++s == ST) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             if (!ok) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
@@ -536,12 +632,12 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             // it arrived on, or, by the other CTA of a pair, from the MMAs that have read it.
             // (A producer that gave up has waited the limit since its last copy.)
             bool drained = true;
-            if (rank == 0) {
-                for (int x = g - 1; x >= 0 && x >= g - ST; --x)
-                    drained &= mbar_wait(&bars[E_FULL + x % ST], (x / ST) & 1, kWaitLimitCycles);
-            } else {
-                for (int x = g > ST ? g - ST : 0; ok && drained && x < g; ++x)
-                    drained = mbar_wait(&bars[E_EMPTY + x % ST], (x / ST) & 1, kWaitLimitCycles);
+            for (int x = min(issued, ST); x > 0 && (rank == 0 || (ok && drained)); --x) {
+                if (--s < 0) {
+                    s = ST - 1;
+                    phase ^= 1;
+                }
+                drained &= mbar_wait(&bars[(rank == 0 ? E_FULL : E_EMPTY) + s], phase, kWaitLimitCycles);
             }
             if (!drained) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
         }
@@ -551,10 +647,13 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
         // the other CTA's warp only zeroes its rows
         constexpr uint32_t idesc = P == P_E4M3 ? idesc_e4m3(CG * EBM, BN)
                                                : idesc_bf16(CG * EBM, BN, P == P_DW, P != P_DX);
-        int g = 0, t = 0;
+        int s = 0, t = 0;
+        uint32_t phase = 0;
         int tails = 0;                                  // bit s: parity of TAIL and READY[s]
         bool ok = !a.stall_test || warp_wait(&bars[E_STALL], 0, a.wait_limit);
-        for (int tile = first; ok && tile < ntiles; tile += stride) {
+        for (int turn = 0; ok; ++turn) {
+            const int tile = deal<P>(turn, first, stride, ntiles);
+            if (tile < 0) break;
             const ETile r = tile_of<P, CG>(a, tab, tile);
             const int kch = (r.kcnt + KB - 1) / KB;
             if (kch == 0) continue;                     // (P_DW: an expert without rows)
@@ -567,13 +666,12 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             ++t;
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
-            for (int kc = 0; kc < kch; ++kc, ++g) {
-                const int s = g % ST;
+            for (int kc = 0; kc < kch; ++kc, phase ^= s + 1 == ST, s = s + 1 == ST ? 0 : s + 1) {
                 const int valid = r.kcnt - kc * KB;     // P_DW: rows of this slice
                 const bool tail = P == P_DW && valid < KB;
                 if (rank != 0 && !tail) continue;
                 if (!warp_wait(&bars[(rank == 0 ? E_FULL : E_TAIL) + s],
-                               (rank == 0 ? g / ST : tails >> s) & 1, a.wait_limit)) {
+                               rank == 0 ? phase : (tails >> s) & 1, a.wait_limit)) {
                     ok = false;
                     break;
                 }
@@ -581,8 +679,8 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                     // rows of this slice past the expert's end: zeros in both operands
                     const int per = (KB - valid) * 8;                // 16-byte pieces per block
                     for (int b = 0; b < (EBM + EBN) / 64; ++b) {
-                        uint8_t *blk = b < EBM / 64 ? sm + L::A_OFF + s * L::AB + b * 8192
-                                                    : sm + L::B_OFF + s * L::BB + (b - EBM / 64) * 8192;
+                        uint8_t *blk = b < EBM / 64 ? sm + s * AB + b * 8192
+                                                    : sm + ST * AB + s * BB + (b - EBM / 64) * 8192;
                         uint4 *z = reinterpret_cast<uint4 *>(blk + valid * 128);
                         for (int x = lane; x < per; x += 32) z[x] = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -601,8 +699,8 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                 }
                 tc_fence_after();
                 if (lane == 0) {
-                    const uint32_t aa = sm_base + L::A_OFF + s * L::AB;
-                    const uint32_t bb = sm_base + L::B_OFF + s * L::BB;
+                    const uint32_t aa = sm_base + s * AB;
+                    const uint32_t bb = sm_base + ST * AB + s * BB;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         // K-major: 32 bytes per step within the 128-byte rows, 8-row groups at
@@ -634,18 +732,20 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
         __syncwarp();
     } else {
         // -------------------------------------------------------------------- epilogue
-        // 32 columns per step: a lane converts its row's values to bf16 and puts them, 16 bytes
-        // at a time and swizzled, into the warp's 2 KB of shared memory, from where 4 lanes
-        // store one row's 64 bytes side by side.  A step is a chain of latencies (TMEM, shared
-        // memory, stores), so four warps per lane quarter work side by side.
+        // A lane converts its row's values, 32 columns at a time, to bf16 and puts them, 16 bytes
+        // at a time and swizzled, into the warp's shared memory, from where NP lanes store one
+        // row's pieces side by side.  That is a chain of latencies (TMEM, shared memory,
+        // stores), so four warps per lane quarter work side by side.
         const int q = warp & 3;                          // TMEM lane quarter: rows 32q ..
         const int quarter = (warp - 2) >> 2;             // a quarter of the columns
         const int rr = q * 32 + lane;                    // row of the tile == TMEM lane
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        uint8_t *stage = sm + L::C_OFF + (warp - 2) * 2048;
+        uint8_t *stage = sm + L::c_off(ST) + (warp - 2) * L::kWarpStage;
         int t = 0;
         bool ok = true;
-        for (int tile = first; tile < ntiles; tile += stride) {
+        for (int turn = 0;; ++turn) {
+            const int tile = deal<P>(turn, first, stride, ntiles);
+            if (tile < 0) break;
             const ETile r = tile_of<P, CG>(a, tab, tile);
             const int m0 = r.m0 + rank * EBM;
             // rows and columns of the tile that this warp stores (none: <= 0)
@@ -676,46 +776,81 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                 tc_fence_after();
             }
             const uint32_t src = tmem + lane_base + acc * BN;
+            constexpr int STEPS = BN / 128, NP = 4 * STEPS;   // pieces of 16 bytes of a lane's row
+            if (P == P_DW && a.partial) {
+                // a slice's sums stay in fp32; each lane stores its row
+                for (int c0 = cbeg; c0 < cend; c0 += 32) {
+                    uint32_t v[32];
+                    __syncwarp();
+                    if (!none) {
+                        tmem_ld32(src + c0, v);
+                        tmem_wait_ld();
+                        reg_fence(v);
+                    }
+                    float *to = a.partial + (((int64_t)r.slice * a.experts + r.e) * a.m + m0 + rr) * a.n +
+                                r.n0 + c0;
 #pragma unroll
-            for (int i = 0; i < BN / 128; ++i) {
-                const int c0 = cbeg + 32 * i, nb = r.n0 + c0;
-                if (c0 >= cend) break;
-                uint32_t v[32];
-                if (!none) {
-                    __syncwarp();                        // the warp-wide TMEM load
-                    tmem_ld32(src + c0, v);
+                    for (int u = 0; u < 32; u += 4)
+                        if (lane < rows && r.n0 + c0 + u < a.n)
+                            *reinterpret_cast<uint4 *>(to + u) =
+                                none ? make_uint4(0u, 0u, 0u, 0u)
+                                     : make_uint4(v[u], v[u + 1], v[u + 2], v[u + 3]);
                 }
-                uint4 pv[4];
-                if constexpr (P == P_E4M3) reinterpret_cast<float *>(stage)[lane] = ws[i];
-                if constexpr (P == P_DX) {
-                    if (a.silu_pre) {                    // 4 lanes a row in, each lane its own out
+            }
+            // the product itself first, where it is wanted, then what becomes of it
+            for (int pass = P == P_FWD && a.pre ? 0 : 1; pass < 2 && cbeg < cend && !(P == P_DW && a.partial);
+                 ++pass) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int row = 8 * u + lane / 4, col = nb + 8 * (lane & 3);
-                            pv[u] = make_uint4(0u, 0u, 0u, 0u);
-                            if (row < rows && col < a.n)
-                                pv[u] = *reinterpret_cast<const uint4 *>(a.silu_pre + (out0 + row) * a.n + col);
+                for (int i = 0; i < STEPS; ++i) {
+                    const int c0 = cbeg + 32 * i, nb = r.n0 + c0;
+                    uint32_t v[32];
+                    if (!none) {
+                        __syncwarp();                    // the warp-wide TMEM load
+                        tmem_ld32(src + c0, v);
+                    }
+                    // what a lane needs of other rows' or columns' lines passes through the place
+                    // that its results take afterwards
+                    uint4 pv[4];
+                    if constexpr (P == P_E4M3) {
+                        reinterpret_cast<float *>(staged<NP>(stage, lane / 4, 4 * i))[lane & 3] = ws[i];
+                    }
+                    if constexpr (P == P_DX) {
+                        if (a.silu_pre) {                // 4 lanes a row in, each lane its own out
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int row = 8 * u + lane / 4, col = nb + 8 * (lane & 3);
+                                pv[u] = make_uint4(0u, 0u, 0u, 0u);
+                                if (row < rows && col < a.n)
+                                    pv[u] = *reinterpret_cast<const uint4 *>(a.silu_pre + (out0 + row) * a.n + col);
+                            }
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                *staged<NP>(stage, 8 * u + lane / 4, 4 * i + (lane & 3)) = pv[u];
+                            __syncwarp();
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) pv[u] = *staged<NP>(stage, lane, 4 * i + u);
                         }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) *staged(stage, 8 * u + lane / 4, lane & 3) = pv[u];
+                    }
+                    if (!none) {
+                        tmem_wait_ld();
+                        reg_fence(v);
+                    }
+                    uint4 o[4];
+                    float4 w4[8];
+                    if constexpr (P == P_E4M3) {
                         __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) pv[u] = *staged(stage, lane, u);
+                        for (int u = 0; u < 8; ++u)
+                            w4[u] = *reinterpret_cast<const float4 *>(staged<NP>(stage, u, 4 * i));
                         __syncwarp();
                     }
+                    convert32<P>(a, none, xs, w4, v, pv, pass == 0, o);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) *staged<NP>(stage, lane, 4 * i + u) = o[u];
                 }
-                if (!none) {
-                    tmem_wait_ld();
-                    reg_fence(v);
-                }
-                uint4 o[4], po[4];
                 __syncwarp();
-                convert32<P>(a, none, xs, reinterpret_cast<const float4 *>(stage), v, pv, o, po);
+                store_rows<NP>(stage, pass == 0 ? a.pre : a.out, out0, rows, r.n0 + cbeg, a.n);
                 __syncwarp();
-                store_rows(stage, o, a.out, out0, rows, nb, a.n);
-                if constexpr (P == P_FWD) {
-                    if (a.pre) store_rows(stage, po, a.pre, out0, rows, nb, a.n);
-                }
             }
             if (!none) {
                 __syncwarp();
@@ -734,6 +869,25 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
         tc_fence_after();
         tmem_give<CG>(tmem, 2 * BN);
     }
+}
+
+// out = the slices' sums added up in order, 8 elements per thread.
+__global__ void __launch_bounds__(256) sum_slices_kernel(const float *__restrict__ partial, int slices,
+                                                         int64_t n, __nv_bfloat16 *__restrict__ out)
+{
+    grid_dep_wait();
+    grid_dep_release();
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= n) return;
+    float f[8] = {};
+#pragma unroll 8
+    for (int s = 0; s < slices; ++s) {
+        const float4 a = reinterpret_cast<const float4 *>(partial + s * n + i)[0];
+        const float4 b = reinterpret_cast<const float4 *>(partial + s * n + i)[1];
+        f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+        f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+    }
+    *reinterpret_cast<uint4 *>(out + i) = pack8(f);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
@@ -798,10 +952,11 @@ int most_pairs(K kern, int smem)
 }
 
 template <int P, int CG>
-cudaError_t run_egemm(const EGemmArgs &a, int64_t most_tiles, cudaStream_t st)
+cudaError_t run_egemm(const EGemmArgs &args, int64_t most_tiles, cudaStream_t st)
 {
-    const int smem = ELayout::TAB_OFF + (3 * a.experts + 1) * 4 + 1024;
-    static_assert(ELayout::TAB_OFF + (3 * kMaxExperts + 1) * 4 + 1024 <= 232448, "shared memory");
+    EGemmArgs a = args;
+    a.stages = ELayout<CG>::stages(a.experts);
+    const int smem = ELayout<CG>::bytes(a.stages, a.experts);
     auto k = expert_gemm_kernel<P, CG>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -813,12 +968,14 @@ cudaError_t run_egemm(const EGemmArgs &a, int64_t most_tiles, cudaStream_t st)
     cfg.blockDim = dim3(kEThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CG;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
+    cfg.numAttrs = CG;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
@@ -835,10 +992,10 @@ cudaError_t run_by_size(const EGemmArgs &a, int64_t rows, cudaStream_t st)
 {
     auto tiles = [&](int cg) {
         const int64_t bm = cg * EBM, bn = cg * EBN, nt = (a.n + bn - 1) / bn;
-        return (P == P_DW ? a.experts * ((a.m + bm - 1) / bm)
+        return (P == P_DW ? (int64_t)a.slices * a.experts * ((a.m + bm - 1) / bm)
                           : most_row_tiles(rows, a.experts, (int)bm)) * nt;
     };
-    const bool pair = P == P_DW ? tiles(2) >= num_sms() / 2
+    const bool pair = P == P_DW ? a.slices == 1 && tiles(2) >= num_sms() / 2
                                 : rows >= (int64_t)a.experts * 192 && tiles(2) >= num_sms() / 2;
     return pair ? run_egemm<P, 2>(a, tiles(2), st) : run_egemm<P, 1>(a, tiles(1), st);
 }
@@ -892,10 +1049,22 @@ cudaError_t launch_expert_proj_dx(const ProjArgs &p, cudaStream_t st)
     return run_by_size<P_DX>(a, p.rows, st);
 }
 
+int expert_dw_slices(int64_t rows, int experts, int k, int n)
+{
+    // Few tiles and many rows: the experts' rows are cut so that the device has work for its SMs
+    // (32768 rows of one expert, 512 x 512: 16 tiles, 174 us in one piece), but to no less than 256
+    // rows on average.  The slices' fp32 sums are at most 148 tiles of 64 KB.
+    const int64_t tiles = (int64_t)experts * ((k + EBM - 1) / EBM) * ((n + EBN - 1) / EBN);
+    int64_t s = 148 / tiles;
+    if (s > 32) s = 32;                                  // (the sum of the parts is a chain)
+    if (s > rows / experts / 256) s = rows / experts / 256;
+    return (int)(s < 1 ? 1 : s);
+}
+
 cudaError_t launch_expert_proj_dw(const ProjArgs &p, cudaStream_t st)
 {
-    if (p.rows <= 0)
-        return cudaMemsetAsync(p.dw, 0, (size_t)p.experts * p.k * p.n * 2, st);
+    const int64_t all = (int64_t)p.experts * p.k * p.n;
+    if (p.rows <= 0) return cudaMemsetAsync(p.dw, 0, (size_t)all * 2, st);
     EGemmArgs a = common(p);
     if (!encode(&a.ta, p.x, false, p.k, p.rows, 0, 64) ||
         !encode(&a.tb, p.dout, false, p.n, p.rows, 0, 64))
@@ -903,7 +1072,12 @@ cudaError_t launch_expert_proj_dw(const ProjArgs &p, cudaStream_t st)
     a.m = p.k;
     a.n = p.n;
     a.out = reinterpret_cast<__nv_bfloat16 *>(p.dw);
-    return run_by_size<P_DW>(a, p.rows, st);
+    a.slices = expert_dw_slices(p.rows, p.experts, p.k, p.n);
+    if (a.slices > 1) a.partial = p.partial;
+    cudaError_t e = run_by_size<P_DW>(a, p.rows, st);
+    if (e != cudaSuccess || a.slices == 1) return e;
+    return launch_pdl(sum_slices_kernel, dim3((unsigned)((all / 8 + 255) / 256)), dim3(256), 0, st,
+                      (const float *)p.partial, a.slices, all, a.out);
 }
 
 }  // namespace hstu

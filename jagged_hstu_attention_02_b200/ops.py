@@ -34,6 +34,7 @@ EXPORTED = ["hstu_attn_fwd_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd_work
             "hstu_expert_sort_workspace_size", "hstu_expert_sort", "hstu_expert_dispatch",
             "hstu_expert_combine", "hstu_expert_combine_bwd", "hstu_expert_proj",
             "hstu_expert_proj_e4m3", "hstu_expert_proj_bwd",
+            "hstu_expert_proj_bwd_workspace_size",
             "hstu_attn_time_thresholds", "hstu_attn_set_stage_events", "hstu_status_string",
             "hstu_attn_version"]
 STAGES = {"fwd_attn": 0, "fwd_norm": 1, "bwd_norm": 2, "bwd_attn": 3}
@@ -111,7 +112,9 @@ def lib():
         L.hstu_expert_combine_bwd.argtypes = [_VP] * 4 + [i64, i32, i64, i32, i32] + [_VP] * 3
         L.hstu_expert_proj.argtypes = [_VP] * 3 + [i64, i32, i32, i32, i32] + [_VP] * 4
         L.hstu_expert_proj_e4m3.argtypes = [_VP] * 5 + [i64, i32, i32, i32, i32] + [_VP] * 3
-        L.hstu_expert_proj_bwd.argtypes = [_VP] * 5 + [i64, i32, i32, i32] + [_VP] * 4
+        L.hstu_expert_proj_bwd.argtypes = [_VP] * 5 + [i64, i32, i32, i32] + [_VP] * 4 + [
+            ctypes.c_size_t, _VP]
+        L.hstu_expert_proj_bwd_workspace_size.argtypes = [i64, i32, i32, i32, sz]
         L.hstu_status_string.restype = ctypes.c_char_p
         L.hstu_status_string.argtypes = [ctypes.c_int]
         L.hstu_attn_version.restype = ctypes.c_int32
@@ -727,7 +730,8 @@ def expert_proj_e4m3(x, x_scales, w, w_scales, offsets, *, silu=False, out=None,
     return out
 
 
-def expert_proj_bwd(dout, x, w, offsets, *, silu_pre=None, grads=None, status=None, stream=None):
+def expert_proj_bwd(dout, x, w, offsets, *, silu_pre=None, grads=None, status=None,
+                    workspace=None, stream=None):
     """(dx, dw) of expert_proj's product.  With silu_pre (x = SiLU(silu_pre)), dx is the gradient
     of silu_pre.  grads: (dx, dw) to write into, None in the place of one not wanted; rows of dx
     of no expert are left as they were."""
@@ -747,9 +751,16 @@ def expert_proj_bwd(dout, x, w, offsets, *, silu_pre=None, grads=None, status=No
         dx, dw = grads
         _expect(dx, "dx", torch.bfloat16, (S, K), x)
         _expect(dw, "dw", torch.bfloat16, (E, K, N), x)
+        if dw is not None and workspace is None:
+            n = ctypes.c_size_t()
+            _check(lib().hstu_expert_proj_bwd_workspace_size(S, E, K, N, ctypes.byref(n)),
+                   "hstu_expert_proj_bwd_workspace_size")
+            if n.value:
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device)
         st = lib().hstu_expert_proj_bwd(_addr(dout), _addr(x), _addr(w), _addr(offsets),
                                         _addr(silu_pre), S, E, K, N, _addr(dx), _addr(dw),
-                                        _addr(status), _raw_stream(x.get_device()))
+                                        _addr(status), _addr(workspace), _bytes(workspace),
+                                        _raw_stream(x.get_device()))
     _check(st, "hstu_expert_proj_bwd")
     return grads
 

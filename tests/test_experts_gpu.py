@@ -445,8 +445,10 @@ def test_proj_bwd(counts, K, N):
 
 
 @pytest.mark.parametrize("counts,K,N", [([399, 1], 72, 6400), ([130, 257, 600, 2, 63], 200, 3336),
-                                        ([1, 0, 63, 64, 65, 127, 129, 300, 2, 5000], 520, 1032)],
-                         ids=["wide", "ragged", "rows"])
+                                        ([1, 0, 63, 64, 65, 127, 129, 300, 2, 5000], 520, 1032),
+                                        ([700, 2, 0, 5300, 3001, 63], 1032, 512),
+                                        ([9000, 1100], 512, 2056)],
+                         ids=["wide", "ragged", "rows", "narrow", "long"])
 def test_products_large_enough_for_pairs_of_blocks(counts, K, N):
     """Few and many rows per expert where the products run on pairs of blocks (256 x 256 tiles):
     rows of no expert hold NaN, and short last slices of the weight gradients' contraction."""
@@ -491,6 +493,25 @@ def test_products_large_enough_for_pairs_of_blocks(counts, K, N):
             assert ((out.t[a:b].double() - r).abs() <= tol + 1e-30).all(), e
         assert (out.t[live:] == 7).all()
         out.check("pairs e4m3")
+
+
+@pytest.mark.parametrize("counts,K,N", [([5000], 64, 128), ([3000, 0, 2003], 72, 136),
+                                        ([20, 9000, 65], 256, 200), ([1100, 1029], 512, 264)],
+                         ids=str)
+def test_weight_gradients_from_parts_of_the_rows(counts, K, N):
+    """Few small matrices and many rows: the contraction is cut into parts that are added up."""
+    x, w, off, S, E = _proj_case(counts, K, N, 3, K + N)
+    do = _rand(9, S, N)
+    do[S - 3:] = float("nan")
+    gw = Guarded((E, K, N), BF)
+    ops.expert_proj_bwd(do, x, w, off, grads=(None, gw.t))
+    for e, (a, b) in enumerate(zip(_np(off), _np(off)[1:])):
+        X, D = x[a:b].double(), do[a:b].double()
+        tol = (X.T @ D).abs() * 2 ** -8 + _dot_tol(int(b - a), X.T.abs() @ D.abs()) + 1e-30
+        assert ((gw.t[e].double() - X.T @ D).abs() <= tol).all(), e
+    gw.check("dw")
+    again = ops.expert_proj_bwd(do, x, w, off, grads=(None, torch.empty_like(w)))[1]
+    assert torch.equal(again, gw.t)
 
 
 def test_proj_without_rows():

@@ -164,8 +164,18 @@ def test_product_refusals():
     for bad in (dict(xs=None), dict(ws=None), dict(K=8), dict(K=72), dict(N=12), dict(ws=_p(8))):
         assert q(**bad) == INVALID, bad
 
-    def bwd(do=_p(), x=_p(), w=_p(), off=_p(), S=4, K=64, N=64, dx=_p(), dw=_p()):
-        return L.hstu_expert_proj_bwd(do, x, w, off, None, S, 2, K, N, dx, dw, None, None)
+    n = ctypes.c_size_t()
+    size = L.hstu_expert_proj_bwd_workspace_size
+    assert size(4, 2, 64, 64, None) == INVALID and size(4, 0, 64, 64, ctypes.byref(n)) == INVALID
+    assert size(4, 2, 64, 64, ctypes.byref(n)) == 0 and n.value == 0
+    assert size(30000, 2, 64, 64, ctypes.byref(n)) == 0 and n.value > 0
+    need = n.value
+
+    def bwd(do=_p(), x=_p(), w=_p(), off=_p(), S=4, K=64, N=64, dx=_p(), dw=_p(), ws=None, nb=0):
+        return L.hstu_expert_proj_bwd(do, x, w, off, None, S, 2, K, N, dx, dw, None, ws, nb, None)
+
+    assert bwd(S=30000) == INVALID and bwd(S=30000, ws=_p(8), nb=need) == INVALID
+    assert bwd(S=30000, ws=_p(), nb=need - 1) == TOO_SMALL
 
     for bad in (dict(do=None), dict(x=None), dict(w=None), dict(off=None), dict(S=-1),
                 dict(K=20), dict(N=20), dict(dx=_p(8)), dict(dw=_p(8))):
