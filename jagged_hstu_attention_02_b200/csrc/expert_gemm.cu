@@ -958,7 +958,7 @@ cudaError_t run_egemm(const EGemmArgs &args, int64_t most_tiles, cudaStream_t st
     a.stages = ELayout<CG>::stages(a.experts);
     const int smem = ELayout<CG>::bytes(a.stages, a.experts);
     auto k = expert_gemm_kernel<P, CG>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<expert_gemm_kernel<P, CG>>(smem);
     if (e != cudaSuccess) return e;
     int64_t tiles = CG == 2 ? most_pairs(k, smem) : num_sms();
     if (most_tiles < tiles) tiles = most_tiles;

@@ -232,20 +232,17 @@ cudaError_t run_sort(const SortArgs &a, cudaStream_t st)
     const size_t smem = (size_t)kSortWarps * a.experts * sizeof(int32_t);
     cudaError_t e;
     if (blocks == 1) {
-        auto k = expert_place_kernel<I, true>;
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_smem<expert_place_kernel<I, true>>(smem);
         if (e != cudaSuccess) return e;
-        return launch_pdl(k, dim3(1), dim3(kSortThreads), smem, st, a);
+        return launch_pdl(expert_place_kernel<I, true>, dim3(1), dim3(kSortThreads), smem, st, a);
     }
-    auto c = expert_count_kernel<I>;
-    e = cudaFuncSetAttribute(c, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_smem<expert_count_kernel<I>>(smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(c, dim3(blocks), dim3(kSortThreads), smem, st, a);
+    e = launch_pdl(expert_count_kernel<I>, dim3(blocks), dim3(kSortThreads), smem, st, a);
     if (e != cudaSuccess) return e;
-    auto k = expert_place_kernel<I, false>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_smem<expert_place_kernel<I, false>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k, dim3(blocks), dim3(kSortThreads), smem, st, a);
+    return launch_pdl(expert_place_kernel<I, false>, dim3(blocks), dim3(kSortThreads), smem, st, a);
 }
 
 // ------------------------------------------------------------------ rows of tokens

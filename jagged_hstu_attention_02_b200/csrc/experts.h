@@ -6,9 +6,37 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "hstu_attn.h"
 
 namespace hstu {
+
+// Lets `kern` use `bytes` of dynamic shared memory.  The attribute is raised once per kernel and
+// device (asking the runtime at every call took a fifth of a small call's time on the host).
+template <auto Kern>
+cudaError_t allow_smem(size_t bytes)
+{
+    constexpr int kMaxDev = 64;
+    static std::atomic<size_t> allowed[kMaxDev];
+    if (bytes <= 48 * 1024) return cudaSuccess;          // every kernel may use that much
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDev && allowed[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    int most = 0;
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, Kern);
+    if (e != cudaSuccess) return e;
+    const size_t room = (size_t)most - fa.sharedSizeBytes;
+    if (bytes > room) return cudaErrorInvalidValue;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDev) allowed[dev].store(room, std::memory_order_release);
+    return cudaSuccess;
+}
 
 // ------------------------------------------------------------------ rmsnorm.cu
 constexpr int kMaxNormWidth = 16384;

@@ -558,13 +558,12 @@ RingPlan ring_plan(int blocks, int64_t stage_bytes, int64_t flight)
     return p;
 }
 
-template <typename K, typename Args>
-cudaError_t launch_norm(K kern, const Args &a, int64_t blocks, int threads, size_t smem, int depth,
-                        cudaStream_t st)
+template <auto Kern, typename Args>
+cudaError_t launch_norm(const Args &a, int64_t blocks, int threads, size_t smem, int depth, cudaStream_t st)
 {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<Kern>(smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)blocks), dim3((unsigned)threads), smem, st, a, depth);
+    return launch_pdl(Kern, dim3((unsigned)blocks), dim3((unsigned)threads), smem, st, a, depth);
 }
 
 template <typename T, bool E4M3, int W>
@@ -577,14 +576,14 @@ cudaError_t run_fwd(const RmsArgs &a, cudaStream_t st)
         // groups keep their rows' alignment: a stride of a multiple of 8 rows
         const int64_t stay = (int64_t)num_sms() * S::shifted_blocks(E4M3) / 8 * 8;
         const size_t maxima = E4M3 && a.group ? (size_t)S::kGroups * ((a.width + a.group - 1) / a.group) * 4 : 0;
-        return launch_norm(rms_norm_kernel<T, W, E4M3, SHIFTED>, a, std::min(blocks, stay),
+        return launch_norm<rms_norm_kernel<T, W, E4M3, SHIFTED>>(a, std::min(blocks, stay),
                            S::kThreads, maxima, 0, st);
     }
     if (blocks <= most)
-        return launch_norm(rms_norm_kernel<T, W, E4M3, DIRECT>, a, blocks, S::kThreads, 0, 0, st);
+        return launch_norm<rms_norm_kernel<T, W, E4M3, DIRECT>>(a, blocks, S::kThreads, 0, 0, st);
     const int64_t stage = (int64_t)a.width * sizeof(T) * (a.resid ? 2 : 1);
     const RingPlan p = ring_plan<W>(S::kFwdBlocks, stage, 64 * 1024);
-    return launch_norm(rms_norm_kernel<T, W, E4M3, RING>, a, (int64_t)num_sms() * p.blocks,
+    return launch_norm<rms_norm_kernel<T, W, E4M3, RING>>(a, (int64_t)num_sms() * p.blocks,
                        S::kThreads, p.smem, p.depth, st);
 }
 
@@ -609,13 +608,13 @@ cudaError_t run_bwd(const RmsBwdArgs &a, cudaStream_t st)
     const size_t parts = S::kGroups > 1 && a.dweight ? (size_t)S::kGroups * a.width * 4 : 0;
     cudaError_t e;
     if (a.width % 8 != 0) {
-        e = launch_norm(rms_norm_bwd_kernel<T, W, SHIFTED>, a, blocks, S::kThreads, parts, 0, st);
+        e = launch_norm<rms_norm_bwd_kernel<T, W, SHIFTED>>(a, blocks, S::kThreads, parts, 0, st);
     } else if (a.rows <= (int64_t)blocks * S::kGroups) {
-        e = launch_norm(rms_norm_bwd_kernel<T, W, DIRECT>, a, blocks, S::kThreads, parts, 0, st);
+        e = launch_norm<rms_norm_bwd_kernel<T, W, DIRECT>>(a, blocks, S::kThreads, parts, 0, st);
     } else {
         const int64_t stage = (int64_t)a.width * sizeof(T) * (a.dsum ? 3 : 2);
         const RingPlan p = ring_plan<W>(S::kBwdBlocks, stage, 160 * 1024);
-        e = launch_norm(rms_norm_bwd_kernel<T, W, RING>, a, blocks, S::kThreads, p.smem, p.depth, st);
+        e = launch_norm<rms_norm_bwd_kernel<T, W, RING>>(a, blocks, S::kThreads, p.smem, p.depth, st);
     }
     if (e != cudaSuccess || !a.dweight) return e;
     return launch_pdl(rms_dweight_kernel, dim3((a.width + 31) / 32), dim3(1024), 0, st,

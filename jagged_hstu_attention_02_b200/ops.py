@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
@@ -452,6 +453,14 @@ def _expect(t, name, dtype, shape, like=None):
         raise ValueError("%s must be on %s" % (name, like.device))
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_size(name, *sizes):
+    """Bytes that the named workspace-size entry point asks for."""
+    n = ctypes.c_size_t()
+    _check(getattr(lib(), name)(*sizes, ctypes.byref(n)), name)
+    return n.value
+
+
 def _expect_slots(slots, like, name="slots"):
     if slots.dim() != 2:
         raise ValueError("%s must be [tokens, choices]" % name)
@@ -537,10 +546,8 @@ def rms_norm_rows_bwd(dy, sum, rstd, weight=None, *, dsum=None, grads=None, work
         _expect(dx, "dx", dy.dtype, dy.shape, dy)
         _expect(dw, "dweight", torch.float32, (width,), dy)
         if dw is not None and workspace is None:
-            n = ctypes.c_size_t()
-            _check(lib().hstu_rms_norm_rows_bwd_workspace_size(rows, width, ctypes.byref(n)),
-                   "hstu_rms_norm_rows_bwd_workspace_size")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dy.device)
+            n = _workspace_size("hstu_rms_norm_rows_bwd_workspace_size", rows, width)
+            workspace = dy.new_empty((n,), dtype=torch.uint8)
         st = lib().hstu_rms_norm_rows_bwd(
             _addr(dy), _addr(sum), _addr(rstd), _addr(weight), _addr(dsum), rows, width, code, _addr(dx),
             _addr(dw), _addr(workspace), _bytes(workspace), _raw_stream(dy.get_device()))
@@ -582,11 +589,9 @@ def expert_sort(expert_ids, num_experts: int, *, status=None, out: Optional[Rout
             _expect(out.offsets, "out.offsets", torch.int64, (num_experts + 1,), expert_ids)
             _expect(out.rows, "out.rows", torch.int64, (T * k,), expert_ids)
         if workspace is None:
-            n = ctypes.c_size_t()
-            _check(lib().hstu_expert_sort_workspace_size(T, k, num_experts, ctypes.byref(n)),
-                   "hstu_expert_sort_workspace_size")
-            if n.value:
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+            n = _workspace_size("hstu_expert_sort_workspace_size", T, k, num_experts)
+            if n:
+                workspace = expert_ids.new_empty((n,), dtype=torch.uint8)
         st = lib().hstu_expert_sort(
             _addr(expert_ids), 1 if expert_ids.dtype == torch.int64 else 0, T, k, num_experts,
             _addr(out.slots), _addr(out.offsets), _addr(out.rows), _addr(status), _addr(workspace),
@@ -752,11 +757,9 @@ def expert_proj_bwd(dout, x, w, offsets, *, silu_pre=None, grads=None, status=No
         _expect(dx, "dx", torch.bfloat16, (S, K), x)
         _expect(dw, "dw", torch.bfloat16, (E, K, N), x)
         if dw is not None and workspace is None:
-            n = ctypes.c_size_t()
-            _check(lib().hstu_expert_proj_bwd_workspace_size(S, E, K, N, ctypes.byref(n)),
-                   "hstu_expert_proj_bwd_workspace_size")
-            if n.value:
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device)
+            n = _workspace_size("hstu_expert_proj_bwd_workspace_size", S, E, K, N)
+            if n:
+                workspace = x.new_empty((n,), dtype=torch.uint8)
         st = lib().hstu_expert_proj_bwd(_addr(dout), _addr(x), _addr(w), _addr(offsets),
                                         _addr(silu_pre), S, E, K, N, _addr(dx), _addr(dw),
                                         _addr(status), _addr(workspace), _bytes(workspace),
