@@ -330,9 +330,10 @@ hstu_status_t hstu_jagged_concat(int32_t n_parts, const void *const *values,
  * Root-mean-square norm of rows with the residual's addition.
  *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * weight
  * x, residual (NULL: none), sum and y are [rows, width] of `dtype`, weight [width] fp32 (NULL:
- * ones); width in 1..16384, rows <= 2^31 - 1.  The statistics and y come from the fp32 h; sum
- * (NULL: not written; required when training with a residual) receives h rounded to dtype, and
- * may be x or residual itself.  rstd [rows] fp32 (NULL: not written) is for the backward.
+ * ones); width in 1..16384, rows <= 2^31 - 1.  The statistics and y come from the fp32 h, summed in
+ * fp32 (values beyond about 1e18 overflow it).  sum (NULL: not written) receives h rounded to dtype,
+ * which the backward reads, and may be x or residual itself.  rstd [rows] fp32 (NULL: not written)
+ * is for the backward.
  *
  * hstu_rms_norm_rows_e4m3 writes y in 8 bits: q [rows, width] e4m3 (values up to 448, rounded to
  * nearest even) and scales [rows, ceil(width / group)] fp32, group = 32, 64 or 128 columns per

@@ -344,6 +344,10 @@ def test_combine_skips_places_outside_and_dispatch_bwd_sums():
     assert dw[0, 1] == 0 and not dw[1].any()
     e = torch.empty(0, 2, dtype=torch.int32, device="cuda")
     assert ops.expert_combine(y, e).shape == (0, 32)
+    assert not ops.expert_combine(y[:0], slots).any()        # no rows at all
+    for width in (7, 520):
+        none = torch.empty(0, width, device="cuda")
+        assert not ops.expert_combine(none, slots, torch.full((3, 2), float("nan"), device="cuda")).any()
 
 
 # ------------------------------------------------------------------ products
@@ -562,6 +566,31 @@ def test_many_experts_and_large_products():
             r = p @ q
             tol = r.abs() * 2 ** -8 + _dot_tol(p.shape[1], p.abs() @ q.abs())
             assert ((got.double() - r).abs() <= tol).all()
+
+
+def test_tensors_of_more_than_two_to_the_31_elements():
+    """Rows whose element offsets pass 32 bits, at both ends of every operator."""
+    S, W, E = 270_000, 8192, 2                       # 2.2e9 elements, 4.4 GB in bf16
+    x = torch.zeros(S, W, dtype=BF, device="cuda")
+    ends = [0, 1, S - 2, S - 1]
+    part = _rand(1, 4, W)
+    x[ends] = part
+    r = ops.rms_norm_rows(x, e4m3=True, group=128)
+    small = ops.rms_norm_rows(part, e4m3=True, group=128)
+    assert torch.equal(r.y[ends].view(torch.uint8), small.y.view(torch.uint8))
+    assert torch.equal(r.scales[ends], small.scales) and not r.y[5].float().any()
+    del r
+    slots = torch.tensor([[S - 1, 0], [1, S - 2]], dtype=torch.int32, device="cuda")
+    out = ops.expert_combine(x, slots)
+    assert torch.equal(out, (torch.stack([part[3].float() + part[0].float(),
+                                          part[1].float() + part[2].float()])).to(BF))
+    w = _rand(2, E, W, 64, scale=W ** -0.5)
+    off = torch.tensor([0, S - 1, S], device="cuda")
+    y = ops.expert_proj(x, w, off)
+    tiny = ops.expert_proj(part, w, torch.tensor([0, 3, 4], device="cuda"))
+    assert torch.equal(y[ends], tiny)
+    xs = ops.expert_dispatch(part[:2], slots, out=x)
+    assert torch.equal(xs[ends], torch.stack([part[0], part[1], part[1], part[0]]))
 
 
 # ------------------------------------------------------------------ the layer
