@@ -6,7 +6,6 @@ path: without the built library, or with tensors not on a CUDA device, calls rai
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -408,49 +407,67 @@ def layer_fwd(x, seq_offsets, num_contextuals, num_targets, timestamps, rel_bias
 # ------------------------------------------------------------------ mixture of experts
 
 F8 = torch.float8_e4m3fn
-_HERE = contextlib.nullcontext()
-# handle of a device's current stream, without the Stream object where torch offers that
+# These calls run for a few microseconds on small batches, so what the host does around them is
+# kept short: one check per tensor, which yields its address, and the stream's handle as an integer.
+_CODES = {torch.float32: HSTU_F32, torch.bfloat16: HSTU_BF16}
+# handle of a device's current stream, and the current device, without the objects and checks
+# around them where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-# These calls run for a few microseconds on small batches, so what the host does around them is
-# kept short: addresses and the stream's handle go to the library as plain integers.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on(t, stream):
-    """Where a call on tensor t allocates and launches: t's device, and `stream` (of that device)
-    or that device's current stream."""
-    dev = t.get_device()
+def _elsewhere(dev, stream):
+    """Whether a call on tensors of device `dev` has to change the device or the stream first."""
+    return dev >= 0 and (stream is not None or dev != _device())
+
+
+def _place(dev, stream):
+    """Context for `stream` (of device `dev`), or for that device's current stream."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device_index != dev:
+        raise ValueError("stream and tensors must be on the same device")
+    return torch.cuda.stream(stream)
+
+
+def _on_cuda(dev):
     if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
-    if stream is not None:
-        if stream.device_index != dev:
-            raise ValueError("stream and tensors must be on the same device")
-        return torch.cuda.stream(stream)
-    if dev == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(dev)
 
 
-def _addr(t):
-    """Address of an optional tensor whose place _expect has checked."""
+def _expect(t, name, dtype, shape, dev):
+    """Address of an optional tensor, checked for its type, shape, device and layout."""
     if t is None:
         return None
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
-
-
-def _expect(t, name, dtype, shape, like=None):
-    """Checks an optional tensor's type, shape and (like: a tensor) device."""
-    if t is None:
-        return
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if like is not None and t.get_device() != like.get_device():
-        raise ValueError("%s must be on %s" % (name, like.device))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the other tensors' device" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _expect_rows(t, name):
+    """(rows, width, dtype code) of a matrix of rows."""
+    if t.dim() != 2:
+        raise ValueError("%s must be [rows, width]" % name)
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s" % t.dtype)
+    rows, width = t.shape
+    return rows, width, code
+
+
+def _expect_status(status, dev):
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise ValueError("status must hold an int32")
+    return _expect(status, "status", torch.int32, status.shape, dev)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -461,19 +478,14 @@ def _workspace_size(name, *sizes):
     return n.value
 
 
-def _expect_slots(slots, like, name="slots"):
-    if slots.dim() != 2:
-        raise ValueError("%s must be [tokens, choices]" % name)
-    shape = slots.shape
-    _expect(slots, name, torch.int32, shape, like)
-    return shape
-
-
-def _expect_status(status, like):
-    if status is not None:
-        if status.numel() < 1:
-            raise ValueError("status must hold an int32")
-        _expect(status, "status", torch.int32, status.shape, like)
+def _workspace(like, given, size, dev):
+    """(address, bytes, tensor) of the workspace: the given one, or a new one of `size` bytes."""
+    if given is None:
+        if size == 0:
+            return None, 0, None
+        given = like.new_empty((size,), dtype=torch.uint8)
+    return _expect(given, "workspace", given.dtype, given.shape, dev), \
+        given.numel() * given.element_size(), given
 
 
 class RmsNorm(NamedTuple):
@@ -490,39 +502,45 @@ def rms_norm_rows(x, weight=None, residual=None, *, eps=1e-5, e4m3=False, group=
     """RMS norm of the rows of h = x (+ residual), times weight (fp32).  e4m3: y in 8 bits with
     one fp32 scale per row (group 0) or per `group` (32, 64, 128) columns, y ~ q * scale.
     training keeps rstd for rms_norm_rows_bwd.  out: a result to write into again."""
-    if x.dim() != 2:
-        raise ValueError("x must be [rows, width]")
-    rows, width = x.shape
-    code = dtype_code(x)
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return rms_norm_rows(x, weight, residual, eps=eps, e4m3=e4m3, group=group,
+                                 training=training, out=out)
+    rows, width, code = _expect_rows(x, "x")
     if group not in (0, 32, 64, 128):
         raise ValueError("group must be 0, 32, 64 or 128")
     if group and not e4m3:
         raise ValueError("group is for the e4m3 output")
-    _expect(weight, "weight", torch.float32, (width,), x)
-    _expect(residual, "residual", x.dtype, x.shape, x)
+    shape, dtype = x.shape, x.dtype
+    px = _expect(x, "x", dtype, shape, dev)
+    pw = _expect(weight, "weight", torch.float32, (width,), dev)
+    pr = _expect(residual, "residual", dtype, shape, dev)
     groups = -(-width // group) if group else 1
-    with _on(x, stream):
-        if out is None:
-            out = RmsNorm(torch.empty_like(x, dtype=F8) if e4m3 else torch.empty_like(x),
-                          x.new_empty((rows, groups), dtype=torch.float32) if e4m3 else None,
-                          torch.empty_like(x) if residual is not None else x,
-                          x.new_empty((rows,), dtype=torch.float32) if training else None)
-        else:
-            _expect(out.y, "out.y", F8 if e4m3 else x.dtype, x.shape, x)
-            _expect(out.scales, "out.scales", torch.float32, (rows, groups), x)
-            _expect(out.sum, "out.sum", x.dtype, x.shape, x)
-            _expect(out.rstd, "out.rstd", torch.float32, (rows,), x)
-            if (e4m3 and out.scales is None) or (training and out.rstd is None):
-                raise ValueError("out lacks scales or rstd")
-        keep = out.sum if residual is not None else None
-        if e4m3:
-            st = lib().hstu_rms_norm_rows_e4m3(
-                _addr(x), _addr(residual), _addr(weight), rows, width, eps, code, group, _addr(out.y),
-                _addr(out.scales), _addr(keep), _addr(out.rstd), _raw_stream(x.get_device()))
-        else:
-            st = lib().hstu_rms_norm_rows(
-                _addr(x), _addr(residual), _addr(weight), rows, width, eps, code, _addr(out.y),
-                _addr(keep), _addr(out.rstd), _raw_stream(x.get_device()))
+    _on_cuda(dev)
+    if out is None:
+        out = RmsNorm(torch.empty_like(x, dtype=F8) if e4m3 else torch.empty_like(x),
+                      x.new_empty((rows, groups), dtype=torch.float32) if e4m3 else None,
+                      x if residual is None else torch.empty_like(x),
+                      x.new_empty((rows,), dtype=torch.float32) if training else None)
+        py, psum = out.y.data_ptr(), out.sum.data_ptr()
+        psc = out.scales.data_ptr() if e4m3 else None
+        pst = out.rstd.data_ptr() if training else None
+    else:
+        py = _expect(out.y, "out.y", F8 if e4m3 else dtype, shape, dev)
+        psc = _expect(out.scales, "out.scales", torch.float32, (rows, groups), dev)
+        psum = _expect(out.sum, "out.sum", dtype, shape, dev)
+        pst = _expect(out.rstd, "out.rstd", torch.float32, (rows,), dev)
+        if (e4m3 and psc is None) or (training and pst is None):
+            raise ValueError("out lacks scales or rstd")
+    if residual is None:
+        psum = None
+    if e4m3:
+        st = lib().hstu_rms_norm_rows_e4m3(px, pr, pw, rows, width, eps, code, group, py, psc, psum,
+                                           pst, _raw_stream(dev))
+    else:
+        st = lib().hstu_rms_norm_rows(px, pr, pw, rows, width, eps, code, py, psum, pst,
+                                      _raw_stream(dev))
     _check(st, "hstu_rms_norm_rows")
     return out
 
@@ -531,32 +549,29 @@ def rms_norm_rows_bwd(dy, sum, rstd, weight=None, *, dsum=None, grads=None, work
                       stream=None):
     """(dx, dweight or None) of rms_norm_rows at its stored sum; dx is the gradient of x and of
     the residual, dsum the gradient that reaches the sum by other ways."""
-    if dy.dim() != 2:
-        raise ValueError("dy must be [rows, width]")
-    rows, width = dy.shape
-    code = dtype_code(dy)
-    _expect(sum, "sum", dy.dtype, dy.shape, dy)
-    _expect(rstd, "rstd", torch.float32, (rows,), dy)
-    _expect(weight, "weight", torch.float32, (width,), dy)
-    _expect(dsum, "dsum", dy.dtype, dy.shape, dy)
-    with _on(dy, stream):
-        if grads is None:
-            grads = (torch.empty_like(dy), None if weight is None else torch.empty_like(weight))
-        dx, dw = grads
-        _expect(dx, "dx", dy.dtype, dy.shape, dy)
-        _expect(dw, "dweight", torch.float32, (width,), dy)
-        if dw is not None and workspace is None:
-            n = _workspace_size("hstu_rms_norm_rows_bwd_workspace_size", rows, width)
-            workspace = dy.new_empty((n,), dtype=torch.uint8)
-        st = lib().hstu_rms_norm_rows_bwd(
-            _addr(dy), _addr(sum), _addr(rstd), _addr(weight), _addr(dsum), rows, width, code, _addr(dx),
-            _addr(dw), _addr(workspace), _bytes(workspace), _raw_stream(dy.get_device()))
-    _check(st, "hstu_rms_norm_rows_bwd")
+    dev = dy.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return rms_norm_rows_bwd(dy, sum, rstd, weight, dsum=dsum, grads=grads,
+                                     workspace=workspace)
+    rows, width, code = _expect_rows(dy, "dy")
+    shape, dtype = dy.shape, dy.dtype
+    pdy = _expect(dy, "dy", dtype, shape, dev)
+    ph = _expect(sum, "sum", dtype, shape, dev)
+    pst = _expect(rstd, "rstd", torch.float32, (rows,), dev)
+    pw = _expect(weight, "weight", torch.float32, (width,), dev)
+    pds = _expect(dsum, "dsum", dtype, shape, dev)
+    _on_cuda(dev)
+    if grads is None:
+        grads = (torch.empty_like(dy), None if weight is None else torch.empty_like(weight))
+    dx, dw = grads
+    pdx = _expect(dx, "dx", dtype, shape, dev)
+    pdw = _expect(dw, "dweight", torch.float32, (width,), dev)
+    need = 0 if dw is None else _workspace_size("hstu_rms_norm_rows_bwd_workspace_size", rows, width)
+    pws, nws, workspace = _workspace(dy, workspace, need, dev)
+    _check(lib().hstu_rms_norm_rows_bwd(pdy, ph, pst, pw, pds, rows, width, code, pdx, pdw, pws, nws,
+                                        _raw_stream(dev)), "hstu_rms_norm_rows_bwd")
     return grads
-
-
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
 
 
 class Routing(NamedTuple):
@@ -572,107 +587,124 @@ def expert_sort(expert_ids, num_experts: int, *, status=None, out: Optional[Rout
                 workspace=None, stream=None) -> Routing:
     """Sorts the pairs of expert_ids [tokens, choices] (int32 or int64; negative: no expert) by
     expert, in the order of the pairs within an expert."""
+    dev = expert_ids.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_sort(expert_ids, num_experts, status=status, out=out,
+                               workspace=workspace)
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be [tokens, choices]")
-    if expert_ids.dtype not in (torch.int32, torch.int64):
+    dtype = expert_ids.dtype
+    if dtype not in (torch.int32, torch.int64):
         raise ValueError("expert_ids must be int32 or int64")
-    T, k = expert_ids.shape
-    _expect_status(status, expert_ids)
-    with _on(expert_ids, stream):
-        dev = expert_ids.device
-        if out is None:
-            out = Routing(torch.empty((T, k), dtype=torch.int32, device=dev),
-                          torch.empty(num_experts + 1, dtype=torch.int64, device=dev),
-                          torch.empty(T * k, dtype=torch.int64, device=dev))
-        else:
-            _expect(out.slots, "out.slots", torch.int32, (T, k), expert_ids)
-            _expect(out.offsets, "out.offsets", torch.int64, (num_experts + 1,), expert_ids)
-            _expect(out.rows, "out.rows", torch.int64, (T * k,), expert_ids)
-        if workspace is None:
-            n = _workspace_size("hstu_expert_sort_workspace_size", T, k, num_experts)
-            if n:
-                workspace = expert_ids.new_empty((n,), dtype=torch.uint8)
-        st = lib().hstu_expert_sort(
-            _addr(expert_ids), 1 if expert_ids.dtype == torch.int64 else 0, T, k, num_experts,
-            _addr(out.slots), _addr(out.offsets), _addr(out.rows), _addr(status), _addr(workspace),
-            _bytes(workspace), _raw_stream(expert_ids.get_device()))
-    _check(st, "hstu_expert_sort")
+    T, k = shape = expert_ids.shape
+    pid = _expect(expert_ids, "expert_ids", dtype, shape, dev)
+    pst = _expect_status(status, dev)
+    _on_cuda(dev)
+    need = _workspace_size("hstu_expert_sort_workspace_size", T, k, num_experts)
+    if out is None:
+        out = Routing(expert_ids.new_empty(shape, dtype=torch.int32),
+                      expert_ids.new_empty((num_experts + 1,), dtype=torch.int64),
+                      expert_ids.new_empty((T * k,), dtype=torch.int64))
+    ps = _expect(out.slots, "out.slots", torch.int32, shape, dev)
+    po = _expect(out.offsets, "out.offsets", torch.int64, (num_experts + 1,), dev)
+    pr = _expect(out.rows, "out.rows", torch.int64, (T * k,), dev)
+    pws, nws, workspace = _workspace(expert_ids, workspace, need, dev)
+    _check(lib().hstu_expert_sort(pid, 1 if dtype == torch.int64 else 0, T, k, num_experts, ps, po,
+                                  pr, pst, pws, nws, _raw_stream(dev)), "hstu_expert_sort")
     return out
+
+
+def _expect_slots(slots, dev):
+    """(tokens, choices, address)."""
+    if slots.dim() != 2:
+        raise ValueError("slots must be [tokens, choices]")
+    T, k = shape = slots.shape
+    return T, k, _expect(slots, "slots", torch.int32, shape, dev)
 
 
 def expert_dispatch(x, slots, *, scales=None, out=None, scales_out=None, stream=None):
     """xs [tokens * choices, ...]: row t of x at every slots[t, j]; with scales (one row of fp32
     per token, e.g. of e4m3 rows) (xs, their scales).  Rows that no slot names are left as they
     were in out."""
-    T, k = _expect_slots(slots, x)
-    if x.dim() < 2 or x.shape[0] != T:
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_dispatch(x, slots, scales=scales, out=out, scales_out=scales_out)
+    T, k, ps = _expect_slots(slots, dev)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) < 2 or shape[0] != T:
         raise ValueError("x must be [tokens, ...] with the slots' tokens")
-    if (scales_out is not None) and scales is None:
+    px = _expect(x, "x", dtype, shape, dev)
+    if scales_out is not None and scales is None:
         raise ValueError("scales_out without scales")
+    psc = pso = None
+    n_scales = 0
     if scales is not None:
         if scales.dim() != 2:
             raise ValueError("scales must be [tokens, n]")
-        _expect(scales, "scales", torch.float32, (T, scales.shape[1]), x)
-    row = x.shape[1:].numel()
-    with _on(x, stream):
-        if out is None:
-            out = torch.empty((T * k,) + tuple(x.shape[1:]), dtype=x.dtype, device=x.device)
-        elif out.dim() < 1 or out.shape[1:] != x.shape[1:]:
-            raise ValueError("out must have rows like x")
-        _expect(out, "out", x.dtype, out.shape, x)
-        if scales is not None:
-            if scales_out is None:
-                scales_out = torch.empty((out.shape[0], scales.shape[1]), dtype=torch.float32,
-                                         device=x.device)
-            _expect(scales_out, "scales_out", torch.float32, (out.shape[0], scales.shape[1]), x)
-        if row:
-            st = lib().hstu_expert_dispatch(
-                _addr(x), row * x.element_size(), _addr(scales),
-                0 if scales is None else scales.shape[1], _addr(slots), T, k, out.shape[0],
-                _addr(out), _addr(scales_out), _raw_stream(x.get_device()))
-            _check(st, "hstu_expert_dispatch")
+        n_scales = scales.shape[1]
+        psc = _expect(scales, "scales", torch.float32, (T, n_scales), dev)
+    _on_cuda(dev)
+    if out is None:
+        out = x.new_empty((T * k,) + tuple(shape[1:]))
+    elif out.shape[1:] != shape[1:]:
+        raise ValueError("out must have rows like x")
+    po = _expect(out, "out", dtype, out.shape, dev)
+    most = out.shape[0]
+    if scales is not None:
+        if scales_out is None:
+            scales_out = scales.new_empty((most, n_scales))
+        pso = _expect(scales_out, "scales_out", torch.float32, (most, n_scales), dev)
+    row = shape[1:].numel()
+    if row:
+        _check(lib().hstu_expert_dispatch(px, row * x.element_size(), psc, n_scales, ps, T, k, most,
+                                          po, pso, _raw_stream(dev)), "hstu_expert_dispatch")
     return out if scales is None else (out, scales_out)
 
 
 def expert_combine(y, slots, weights=None, *, residual=None, out=None, stream=None):
     """out [tokens, width] = residual + sum over j of weights[:, j] * y[slots[:, j]]."""
-    T, k = _expect_slots(slots, y)
-    if y.dim() != 2:
-        raise ValueError("y must be [rows, width]")
-    shape = (T, y.shape[1])
-    code = dtype_code(y)
-    _expect(weights, "weights", torch.float32, (T, k), y)
-    _expect(residual, "residual", y.dtype, shape, y)
-    _expect(out, "out", y.dtype, shape, y)
-    with _on(y, stream):
-        if out is None:
-            out = y.new_empty(shape)
-        st = lib().hstu_expert_combine(
-            _addr(y), _addr(slots), _addr(weights), _addr(residual), T, k, y.shape[0], y.shape[1],
-            code, _addr(out), _raw_stream(y.get_device()))
-    _check(st, "hstu_expert_combine")
+    dev = y.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_combine(y, slots, weights, residual=residual, out=out)
+    T, k, ps = _expect_slots(slots, dev)
+    rows, width, code = _expect_rows(y, "y")
+    shape, dtype = (T, width), y.dtype
+    py = _expect(y, "y", dtype, y.shape, dev)
+    pw = _expect(weights, "weights", torch.float32, (T, k), dev)
+    pr = _expect(residual, "residual", dtype, shape, dev)
+    _on_cuda(dev)
+    if out is None:
+        out = y.new_empty(shape)
+    po = _expect(out, "out", dtype, shape, dev)
+    _check(lib().hstu_expert_combine(py, ps, pw, pr, T, k, rows, width, code, po, _raw_stream(dev)),
+           "hstu_expert_combine")
     return out
 
 
 def expert_combine_bwd(dout, y, slots, weights=None, *, grads=None, stream=None):
     """(dy, dweights or None) of expert_combine; rows of dy that no slot names are left as they
     were.  The residual's gradient is dout itself."""
-    T, k = _expect_slots(slots, y)
-    if y.dim() != 2:
-        raise ValueError("y must be [rows, width]")
-    code = dtype_code(y)
-    _expect(dout, "dout", y.dtype, (T, y.shape[1]), y)
-    _expect(weights, "weights", torch.float32, (T, k), y)
-    with _on(y, stream):
-        if grads is None:
-            grads = (torch.empty_like(y), None if weights is None else torch.empty_like(weights))
-        dy, dw = grads
-        _expect(dy, "dy", y.dtype, y.shape, y)
-        _expect(dw, "dweights", torch.float32, (T, k), y)
-        st = lib().hstu_expert_combine_bwd(
-            _addr(dout), _addr(y), _addr(slots), _addr(weights), T, k, y.shape[0], y.shape[1], code,
-            _addr(dy), _addr(dw), _raw_stream(y.get_device()))
-    _check(st, "hstu_expert_combine_bwd")
+    dev = y.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_combine_bwd(dout, y, slots, weights, grads=grads)
+    T, k, ps = _expect_slots(slots, dev)
+    rows, width, code = _expect_rows(y, "y")
+    dtype = y.dtype
+    py = _expect(y, "y", dtype, y.shape, dev)
+    pdo = _expect(dout, "dout", dtype, (T, width), dev)
+    pw = _expect(weights, "weights", torch.float32, (T, k), dev)
+    _on_cuda(dev)
+    if grads is None:
+        grads = (torch.empty_like(y), None if weights is None else torch.empty_like(weights))
+    dy, dw = grads
+    pdy = _expect(dy, "dy", dtype, y.shape, dev)
+    pdw = _expect(dw, "dweights", torch.float32, (T, k), dev)
+    _check(lib().hstu_expert_combine_bwd(pdo, py, ps, pw, T, k, rows, width, code, pdy, pdw,
+                                         _raw_stream(dev)), "hstu_expert_combine_bwd")
     return grads
 
 
@@ -681,31 +713,35 @@ def expert_dispatch_bwd(dxs, slots, *, out=None, stream=None):
     return expert_combine(dxs, slots, out=out, stream=stream)
 
 
-def _expect_experts(offsets, experts, like):
-    _expect(offsets, "offsets", torch.int64, (experts + 1,), like)
+def _expect_proj(x, w):
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, d_in] and w [experts, ., .]")
 
 
 def expert_proj(x, w, offsets, *, silu=False, pre=None, out=None, status=None, stream=None):
     """out [rows, d_out]: each expert's rows offsets[e] .. offsets[e+1] of x [rows, d_in] (bf16)
     times w[e] of [experts, d_in, d_out], SiLU after it when silu (the product itself then to
     pre, when given).  Rows of no expert are left as they were in out."""
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError("x must be [rows, d_in] and w [experts, d_in, d_out]")
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_proj(x, w, offsets, silu=silu, pre=pre, out=out, status=status)
+    _expect_proj(x, w)
     S, K = x.shape
     E, N = w.shape[0], w.shape[2]
-    _expect(x, "x", torch.bfloat16, (S, K))
-    _expect(w, "w", torch.bfloat16, (E, K, N), x)
-    _expect_experts(offsets, E, x)
-    _expect(pre, "pre", torch.bfloat16, (S, N), x)
-    _expect(out, "out", torch.bfloat16, (S, N), x)
-    _expect_status(status, x)
-    with _on(x, stream):
-        if out is None:
-            out = x.new_empty((S, N))
-        st = lib().hstu_expert_proj(_addr(x), _addr(w), _addr(offsets), S, E, K, N,
-                                    1 if silu else 0, _addr(out), _addr(pre), _addr(status),
-                                    _raw_stream(x.get_device()))
-    _check(st, "hstu_expert_proj")
+    if pre is not None and not silu:
+        raise ValueError("pre is for the product ahead of the SiLU")
+    px = _expect(x, "x", torch.bfloat16, (S, K), dev)
+    pw = _expect(w, "w", torch.bfloat16, (E, K, N), dev)
+    pof = _expect(offsets, "offsets", torch.int64, (E + 1,), dev)
+    pp = _expect(pre, "pre", torch.bfloat16, (S, N), dev)
+    pst = _expect_status(status, dev)
+    _on_cuda(dev)
+    if out is None:
+        out = x.new_empty((S, N))
+    po = _expect(out, "out", torch.bfloat16, (S, N), dev)
+    _check(lib().hstu_expert_proj(px, pw, pof, S, E, K, N, 1 if silu else 0, po, pp, pst,
+                                  _raw_stream(dev)), "hstu_expert_proj")
     return out
 
 
@@ -713,25 +749,26 @@ def expert_proj_e4m3(x, x_scales, w, w_scales, offsets, *, silu=False, out=None,
                      stream=None):
     """expert_proj of e4m3 rows x [rows, d_in] with scales (one fp32 per row) and e4m3 weights w
     [experts, d_out, d_in] with scales [experts, d_out]; out is bf16."""
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError("x must be [rows, d_in] and w [experts, d_out, d_in]")
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_proj_e4m3(x, x_scales, w, w_scales, offsets, silu=silu, out=out,
+                                    status=status)
+    _expect_proj(x, w)
     S, K = x.shape
     E, N = w.shape[0], w.shape[1]
-    _expect(x, "x", F8, (S, K))
-    _expect(w, "w", F8, (E, N, K), x)
-    _expect(x_scales, "x_scales", torch.float32,
-            (S, 1) if x_scales.dim() == 2 else (S,), x)
-    _expect(w_scales, "w_scales", torch.float32, (E, N), x)
-    _expect_experts(offsets, E, x)
-    _expect(out, "out", torch.bfloat16, (S, N), x)
-    _expect_status(status, x)
-    with _on(x, stream):
-        if out is None:
-            out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
-        st = lib().hstu_expert_proj_e4m3(_addr(x), _addr(x_scales), _addr(w), _addr(w_scales),
-                                         _addr(offsets), S, E, K, N, 1 if silu else 0, _addr(out),
-                                         _addr(status), _raw_stream(x.get_device()))
-    _check(st, "hstu_expert_proj_e4m3")
+    px = _expect(x, "x", F8, (S, K), dev)
+    pw = _expect(w, "w", F8, (E, N, K), dev)
+    pxs = _expect(x_scales, "x_scales", torch.float32, (S, 1) if x_scales.dim() == 2 else (S,), dev)
+    pws = _expect(w_scales, "w_scales", torch.float32, (E, N), dev)
+    pof = _expect(offsets, "offsets", torch.int64, (E + 1,), dev)
+    pst = _expect_status(status, dev)
+    _on_cuda(dev)
+    if out is None:
+        out = x.new_empty((S, N), dtype=torch.bfloat16)
+    po = _expect(out, "out", torch.bfloat16, (S, N), dev)
+    _check(lib().hstu_expert_proj_e4m3(px, pxs, pw, pws, pof, S, E, K, N, 1 if silu else 0, po, pst,
+                                       _raw_stream(dev)), "hstu_expert_proj_e4m3")
     return out
 
 
@@ -740,31 +777,30 @@ def expert_proj_bwd(dout, x, w, offsets, *, silu_pre=None, grads=None, status=No
     """(dx, dw) of expert_proj's product.  With silu_pre (x = SiLU(silu_pre)), dx is the gradient
     of silu_pre.  grads: (dx, dw) to write into, None in the place of one not wanted; rows of dx
     of no expert are left as they were."""
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError("x must be [rows, d_in] and w [experts, d_in, d_out]")
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_proj_bwd(dout, x, w, offsets, silu_pre=silu_pre, grads=grads,
+                                   status=status, workspace=workspace)
+    _expect_proj(x, w)
     S, K = x.shape
     E, N = w.shape[0], w.shape[2]
-    _expect(x, "x", torch.bfloat16, (S, K))
-    _expect(w, "w", torch.bfloat16, (E, K, N), x)
-    _expect(dout, "dout", torch.bfloat16, (S, N), x)
-    _expect(silu_pre, "silu_pre", torch.bfloat16, (S, K), x)
-    _expect_experts(offsets, E, x)
-    _expect_status(status, x)
-    with _on(x, stream):
-        if grads is None:
-            grads = (torch.empty_like(x), torch.empty_like(w))
-        dx, dw = grads
-        _expect(dx, "dx", torch.bfloat16, (S, K), x)
-        _expect(dw, "dw", torch.bfloat16, (E, K, N), x)
-        if dw is not None and workspace is None:
-            n = _workspace_size("hstu_expert_proj_bwd_workspace_size", S, E, K, N)
-            if n:
-                workspace = x.new_empty((n,), dtype=torch.uint8)
-        st = lib().hstu_expert_proj_bwd(_addr(dout), _addr(x), _addr(w), _addr(offsets),
-                                        _addr(silu_pre), S, E, K, N, _addr(dx), _addr(dw),
-                                        _addr(status), _addr(workspace), _bytes(workspace),
-                                        _raw_stream(x.get_device()))
-    _check(st, "hstu_expert_proj_bwd")
+    px = _expect(x, "x", torch.bfloat16, (S, K), dev)
+    pw = _expect(w, "w", torch.bfloat16, (E, K, N), dev)
+    pdo = _expect(dout, "dout", torch.bfloat16, (S, N), dev)
+    pp = _expect(silu_pre, "silu_pre", torch.bfloat16, (S, K), dev)
+    pof = _expect(offsets, "offsets", torch.int64, (E + 1,), dev)
+    pst = _expect_status(status, dev)
+    _on_cuda(dev)
+    if grads is None:
+        grads = (torch.empty_like(x), torch.empty_like(w))
+    dx, dw = grads
+    pdx = _expect(dx, "dx", torch.bfloat16, (S, K), dev)
+    pdw = _expect(dw, "dw", torch.bfloat16, (E, K, N), dev)
+    need = 0 if dw is None else _workspace_size("hstu_expert_proj_bwd_workspace_size", S, E, K, N)
+    pws, nws, workspace = _workspace(x, workspace, need, dev)
+    _check(lib().hstu_expert_proj_bwd(pdo, px, pw, pof, pp, S, E, K, N, pdx, pdw, pst, pws, nws,
+                                      _raw_stream(dev)), "hstu_expert_proj_bwd")
     return grads
 
 
@@ -775,40 +811,45 @@ def expert_layer_fwd(x, residual, norm_weight, expert_ids, gates, w_in, w_out, *
     [T, choices] and added to h.  w_in [E, d_model, d_ff], or (e4m3 [E, d_ff, d_model], scales
     [E, d_ff]) for the 8-bit product (inference); w_out [E, d_ff, d_model].  Returns dict(o, sum,
     rstd, routing, xs, pre, z, y); expert_layer_bwd takes it after training=True."""
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_layer_fwd(x, residual, norm_weight, expert_ids, gates, w_in, w_out,
+                                    ln_eps=ln_eps, training=training, status=status)
     eight = isinstance(w_in, (tuple, list))
     if eight and training:
         raise ValueError("the 8-bit product has no backward")
     E = w_out.shape[0]
-    n = rms_norm_rows(x, norm_weight, residual, eps=ln_eps, e4m3=eight, training=training,
-                      stream=stream)
-    r = expert_sort(expert_ids, E, status=status, stream=stream)
+    n = rms_norm_rows(x, norm_weight, residual, eps=ln_eps, e4m3=eight, training=training)
+    r = expert_sort(expert_ids, E, status=status)
     pre = None
     if eight:
-        xs, sc = expert_dispatch(n.y, r.slots, scales=n.scales, stream=stream)
-        z = expert_proj_e4m3(xs, sc, w_in[0], w_in[1], r.offsets, silu=True, status=status,
-                             stream=stream)
+        xs, sc = expert_dispatch(n.y, r.slots, scales=n.scales)
+        z = expert_proj_e4m3(xs, sc, w_in[0], w_in[1], r.offsets, silu=True, status=status)
     else:
-        xs = expert_dispatch(n.y, r.slots, stream=stream)
+        xs = expert_dispatch(n.y, r.slots)
         if training:
-            with _on(x, stream):
-                pre = torch.empty((xs.shape[0], w_in.shape[2]), dtype=x.dtype, device=x.device)
-        z = expert_proj(xs, w_in, r.offsets, silu=True, pre=pre, status=status, stream=stream)
-    y = expert_proj(z, w_out, r.offsets, status=status, stream=stream)
-    o = expert_combine(y, r.slots, gates, residual=n.sum, stream=stream)
+            pre = x.new_empty((xs.shape[0], w_in.shape[2]))
+        z = expert_proj(xs, w_in, r.offsets, silu=True, pre=pre, status=status)
+    y = expert_proj(z, w_out, r.offsets, status=status)
+    o = expert_combine(y, r.slots, gates, residual=n.sum)
     return dict(o=o, sum=n.sum, rstd=n.rstd, routing=r, xs=xs, pre=pre, z=z, y=y)
 
 
 def expert_layer_bwd(do, saved, norm_weight, gates, w_in, w_out, *, status=None, stream=None):
     """Gradients of expert_layer_fwd(..., training=True), whose result is `saved`: dict(dx (of x
     and of residual alike), dnorm_weight, dgates, dw_in, dw_out)."""
+    dev = do.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return expert_layer_bwd(do, saved, norm_weight, gates, w_in, w_out, status=status)
     r = saved["routing"]
-    dy, dgates = expert_combine_bwd(do, saved["y"], r.slots, gates, stream=stream)
+    dy, dgates = expert_combine_bwd(do, saved["y"], r.slots, gates)
     dpre, dw_out = expert_proj_bwd(dy, saved["z"], w_out, r.offsets, silu_pre=saved["pre"],
-                                   status=status, stream=stream)
-    dxs, dw_in = expert_proj_bwd(dpre, saved["xs"], w_in, r.offsets, status=status, stream=stream)
-    dn = expert_dispatch_bwd(dxs, r.slots, stream=stream)
-    dx, dnw = rms_norm_rows_bwd(dn, saved["sum"], saved["rstd"], norm_weight, dsum=do,
-                                stream=stream)
+                                   status=status)
+    dxs, dw_in = expert_proj_bwd(dpre, saved["xs"], w_in, r.offsets, status=status)
+    dn = expert_dispatch_bwd(dxs, r.slots)
+    dx, dnw = rms_norm_rows_bwd(dn, saved["sum"], saved["rstd"], norm_weight, dsum=do)
     return dict(dx=dx, dnorm_weight=dnw, dgates=dgates, dw_in=dw_in, dw_out=dw_out)
 
 
