@@ -753,7 +753,7 @@ hstu_status_t hstu_expert_proj_bwd_workspace_size(int64_t rows, int32_t num_expe
                                                   int32_t d_out, size_t *bytes)
 {
     if (!bytes || !proj_shape_ok(rows, num_experts, d_in, d_out, 8)) return HSTU_ERR_INVALID_ARGUMENT;
-    const int slices = expert_dw_slices(rows, num_experts, d_in, d_out);
+    const int slices = expert_dw_plan(rows, num_experts, d_in, d_out).slices;
     *bytes = slices > 1 ? (size_t)slices * num_experts * d_in * d_out * 4 : 0;
     return HSTU_OK;
 }

@@ -6,14 +6,23 @@
 //   P_DX    dx_s = (dout_s W_e^T) (.) SiLU'(pre_s)
 //   P_DW    dW_e = X_e^T dOut_e        contraction over the expert's rows
 //
-// Persistent CTAs take 128 x BN output tiles; a tile lies in one expert.  The host never reads
-// the offsets: every CTA sums up the experts' row tiles in shared memory at its start and finds
-// a tile's expert by bisection.  Warp 0 streams 128-byte-wide slices of both operands through a
-// TMA ring (128-byte swizzle), warp 1 issues tcgen05.mma into one of two TMEM accumulators,
-// eight warps read the other accumulator back and store it.  Rows of a tile past the
-// expert's end hold another expert's rows (or nothing): they are computed, not stored.  In P_DW
-// they would enter the sums, so the MMA warp zeroes them in shared memory first.
-// Every wait is bounded.
+// Persistent: a CTA takes 128 x 128 output tiles (CG = 1), or a pair of CTAs 256 x 256 ones with
+// cta_group::2 (CG = 2); a tile lies in one expert.  The host never reads the offsets: every CTA
+// sums up the experts' row tiles in shared memory at its start and finds a tile's expert by
+// bisection.  Warp 0 streams 128-byte-wide slices of both operands through a TMA ring (128-byte
+// swizzle), warp 1 issues tcgen05.mma into one of two TMEM accumulators, sixteen warps read the
+// other accumulator back and store it.  Rows of a tile past the expert's end hold another
+// expert's rows (or nothing): they are computed, not stored.  In P_DW they would enter the sums, so
+// the MMA warp zeroes them in shared memory first.  Every wait is bounded.
+//
+// What bounds it: with 256 x 256 tiles each slice brings 32 KB per CTA from L2 for 512 cycles of
+// MMAs, and that traffic (with the results going the other way) paces the loop: 740 to 800 cycles
+// per slice.  8192^3 bf16 takes 0.71 ms in a burst (1.55 PFLOP/s, 0.96 of the measured peak) and
+// 0.87 ms at the power limit; e4m3 0.37 ms (2.96 PFLOP/s).  Few rows per expert: the weights' bytes
+// (256 rows of 64 experts, 1024 x 2048: 46 us, 5.7 TB/s).  Measured and dropped: 128 x 256 tiles of
+// one CTA (0.94 PFLOP/s: shared memory's bandwidth), A kept in shared memory for all column tiles of
+// a short contraction (too few stages left for B: 46 -> 64 us), the second CTA's warp reporting every
+// slice to the leader (a cluster-scope release per slice: 0.57 PFLOP/s).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -985,18 +994,17 @@ int64_t most_row_tiles(int64_t rows, int experts, int tile)
     return rows / tile + (rows < experts ? rows : experts);
 }
 
-// Pairs of CTAs (256 x 256 tiles) read each operand half as often and reach the higher rate;
-// single CTAs (128 x 128) waste less on short experts and fill the device with fewer tiles.
+// Pairs of CTAs (256 x 256 tiles) read each operand half as often and reach the higher rate; single
+// CTAs (128 x 128) waste less on experts of few rows, and fill the device with fewer tiles.  32
+// experts, 1024 x 1024 bf16, single against pair: 64 rows each 18.7 against 22.8 us, 128 rows 24.6
+// against 24.9, 192 rows 30.7 against 29.7, 768 rows 84 against 64.
 template <int P>
 cudaError_t run_by_size(const EGemmArgs &a, int64_t rows, cudaStream_t st)
 {
     auto tiles = [&](int cg) {
-        const int64_t bm = cg * EBM, bn = cg * EBN, nt = (a.n + bn - 1) / bn;
-        return (P == P_DW ? (int64_t)a.slices * a.experts * ((a.m + bm - 1) / bm)
-                          : most_row_tiles(rows, a.experts, (int)bm)) * nt;
+        return most_row_tiles(rows, a.experts, cg * EBM) * ((a.n + cg * EBN - 1) / (cg * EBN));
     };
-    const bool pair = P == P_DW ? a.slices == 1 && tiles(2) >= num_sms() / 2
-                                : rows >= (int64_t)a.experts * 192 && tiles(2) >= num_sms() / 2;
+    const bool pair = rows >= (int64_t)a.experts * 160 && tiles(2) >= num_sms() / 2;
     return pair ? run_egemm<P, 2>(a, tiles(2), st) : run_egemm<P, 1>(a, tiles(1), st);
 }
 
@@ -1049,16 +1057,28 @@ cudaError_t launch_expert_proj_dx(const ProjArgs &p, cudaStream_t st)
     return run_by_size<P_DX>(a, p.rows, st);
 }
 
-int expert_dw_slices(int64_t rows, int experts, int k, int n)
+// Tiles of the weights' gradient for CTAs (cg = 1) or pairs (cg = 2).
+static int64_t dw_tiles(int cg, int experts, int k, int n)
 {
-    // Few tiles and many rows: the experts' rows are cut so that the device has work for its SMs
-    // (32768 rows of one expert, 512 x 512: 16 tiles, 174 us in one piece), but to no less than 256
-    // rows on average.  The slices' fp32 sums are at most 148 tiles of 64 KB.
-    const int64_t tiles = (int64_t)experts * ((k + EBM - 1) / EBM) * ((n + EBN - 1) / EBN);
-    int64_t s = 148 / tiles;
-    if (s > 32) s = 32;                                  // (the sum of the parts is a chain)
-    if (s > rows / experts / 256) s = rows / experts / 256;
-    return (int)(s < 1 ? 1 : s);
+    return (int64_t)experts * ((k + cg * EBM - 1) / (cg * EBM)) * ((n + cg * EBN - 1) / (cg * EBN));
+}
+
+// Few tiles and many rows: the experts' rows are cut so that the device has work for its SMs, but
+// to no less than 256 rows on average.  The slices' fp32 sums are at most 148 tiles of 64 KB.
+DwPlan expert_dw_plan(int64_t rows, int experts, int k, int n)
+{
+    constexpr int64_t kSms = 148;            // (the workspace's size must not depend on the device)
+    const int64_t t1 = dw_tiles(1, experts, k, n), t2 = dw_tiles(2, experts, k, n);
+    const int64_t most = rows / experts / 256;
+    DwPlan p;
+    // pairs where they fill the device, or where parts of the rows do; matrices below 192 leave
+    // most of a pair's tile empty
+    p.pair = t2 >= kSms / 2 || (k >= 192 && n >= 192 && kSms / 2 / t2 >= 2 && most >= 2);
+    int64_t s = p.pair ? kSms / 2 / t2 : kSms / t1;
+    if (s > 32) s = 32;                      // (the sum of the parts is a chain)
+    if (s > most) s = most;
+    p.slices = (int)(s < 1 ? 1 : s);
+    return p;
 }
 
 cudaError_t launch_expert_proj_dw(const ProjArgs &p, cudaStream_t st)
@@ -1072,9 +1092,11 @@ cudaError_t launch_expert_proj_dw(const ProjArgs &p, cudaStream_t st)
     a.m = p.k;
     a.n = p.n;
     a.out = reinterpret_cast<__nv_bfloat16 *>(p.dw);
-    a.slices = expert_dw_slices(p.rows, p.experts, p.k, p.n);
+    const DwPlan plan = expert_dw_plan(p.rows, p.experts, p.k, p.n);
+    a.slices = plan.slices;
     if (a.slices > 1) a.partial = p.partial;
-    cudaError_t e = run_by_size<P_DW>(a, p.rows, st);
+    const int64_t tiles = a.slices * dw_tiles(plan.pair ? 2 : 1, p.experts, p.k, p.n);
+    cudaError_t e = plan.pair ? run_egemm<P_DW, 2>(a, tiles, st) : run_egemm<P_DW, 1>(a, tiles, st);
     if (e != cudaSuccess || a.slices == 1) return e;
     return launch_pdl(sum_slices_kernel, dim3((unsigned)((all / 8 + 255) / 256)), dim3(256), 0, st,
                       (const float *)p.partial, a.slices, all, a.out);

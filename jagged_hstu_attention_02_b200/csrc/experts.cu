@@ -27,7 +27,9 @@ namespace {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortOneBlock = 2048;     // pairs that one block sorts by itself
+// Pairs that one block sorts by itself: 2048 take 6.8 us (7.0 with two launches over several
+// blocks), 4096 10.7 (7.0), 1024 5.2 (4.9), 512 3.9 (3.9).
+constexpr int kSortOneBlock = 2048;
 constexpr int kSortMaxBlocks = 148;
 constexpr int kBatch = 4;               // ids per lane fetched at a time
 
@@ -335,28 +337,40 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     }
 }
 
-// Narrow rows: 2^shift lanes per (token, choice) pair, one piece each, so that a warp moves
-// several pairs (131072 tokens of 32 bytes, 8 choices: 96 us with a warp per token).
+// Narrow rows (up to 16 pieces): 2^shift lanes per (token, choice) pair, one piece each, 4 pairs
+// per lane.  262144 pairs, against a warp per token: 64-byte rows 35 us there, 256-byte rows 37
+// against 31, 512-byte rows (which the other kernel takes) 41 against 59.
 template <typename V>
 __global__ void __launch_bounds__(256)
     expert_dispatch_narrow_kernel(const __grid_constant__ DispatchArgs a, int shift)
 {
     grid_dep_wait();
     grid_dep_release();
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t pair = id >> shift;
-    if (pair >= a.tokens * a.choices) return;
-    const int c = (int)(id & ((1 << shift) - 1)), lanes = 1 << shift;
+    const int lanes = 1 << shift, c = threadIdx.x & (lanes - 1);
+    const int64_t n = a.tokens * a.choices, step = 256 >> shift;
+    const int64_t first = (int64_t)blockIdx.x * 4 * step + (threadIdx.x >> shift);
     const int per = (int)(a.row_bytes / (int64_t)sizeof(V));
-    const int s = a.slots[pair];
-    if (s < 0 || s >= a.max_rows) return;
-    const int64_t t = (uint32_t)pair / (uint32_t)a.choices;        // tokens * choices < 2^31
-    if (c < per)
-        reinterpret_cast<V *>(a.out + (int64_t)s * a.row_bytes)[c] =
-            reinterpret_cast<const V *>(a.x + t * a.row_bytes)[c];
-    if (a.scales)
-        for (int g = c; g < a.n_scales; g += lanes)
-            a.scales_out[(int64_t)s * a.n_scales + g] = a.scales[t * a.n_scales + g];
+    int s[4];
+    uint32_t t[4];
+    V v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t pair = first + u * step;
+        s[u] = pair < n ? a.slots[pair] : -1;
+        if (s[u] >= a.max_rows) s[u] = -1;
+        t[u] = (uint32_t)pair / (uint32_t)a.choices;           // tokens * choices < 2^31
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (s[u] >= 0 && c < per) v[u] = reinterpret_cast<const V *>(a.x + (int64_t)t[u] * a.row_bytes)[c];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        if (s[u] < 0) continue;
+        if (c < per) reinterpret_cast<V *>(a.out + (int64_t)s[u] * a.row_bytes)[c] = v[u];
+        if (a.scales)
+            for (int g = c; g < a.n_scales; g += lanes)
+                a.scales_out[(int64_t)s[u] * a.n_scales + g] = a.scales[(int64_t)t[u] * a.n_scales + g];
+    }
 }
 
 template <typename V>
@@ -366,9 +380,10 @@ cudaError_t run_dispatch(const DispatchArgs &a, cudaStream_t st)
     if (per <= 16) {
         int shift = 0;
         while ((1 << shift) < per) ++shift;
-        const int64_t threads = (a.tokens * a.choices) << shift;
-        return launch_pdl(expert_dispatch_narrow_kernel<V>, dim3((unsigned)((threads + 255) / 256)),
-                          dim3(256), 0, st, a, shift);
+        const int64_t per_block = 4 * (256 >> shift);
+        return launch_pdl(expert_dispatch_narrow_kernel<V>,
+                          dim3((unsigned)((a.tokens * a.choices + per_block - 1) / per_block)), dim3(256),
+                          0, st, a, shift);
     }
     const int wpr = warps_per_row((a.row_bytes + 15) / 16, sizeof(V) == 16 ? 4 : 1);
     const int tokens = kRowWarps / wpr;

@@ -124,15 +124,20 @@ struct ProjArgs {
     const void *dout;           // backward: [rows, n]
     const void *silu_pre;       // backward: [rows, k] or null
     void *dx, *dw;              // backward: [rows, k], [experts, k, n]
-    float *partial;             // dw: expert_dw_slices(...) x experts x k x n floats when > 1
+    float *partial;             // dw: expert_dw_plan(...).slices x experts x k x n floats when > 1
     int32_t *status;
     long long wait_limit;
     int stall_test;
 };
 cudaError_t launch_expert_proj(const ProjArgs &a, bool e4m3, cudaStream_t st);
 cudaError_t launch_expert_proj_dx(const ProjArgs &a, cudaStream_t st);
-// Parts that the experts' rows are cut into for the weights' gradient.
-int expert_dw_slices(int64_t rows, int experts, int k, int n);
+// How the weights' gradient runs: by pairs of CTAs or single ones, and the parts that the
+// experts' rows are cut into.
+struct DwPlan {
+    bool pair;
+    int slices;
+};
+DwPlan expert_dw_plan(int64_t rows, int experts, int k, int n);
 cudaError_t launch_expert_proj_dw(const ProjArgs &a, cudaStream_t st);
 
 }  // namespace hstu
