@@ -787,7 +787,9 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             const uint32_t src = tmem + lane_base + acc * BN;
             constexpr int STEPS = BN / 128, NP = 4 * STEPS;   // pieces of 16 bytes of a lane's row
             if (P == P_DW && a.partial) {
-                // a slice's sums stay in fp32; each lane stores its row
+                // a slice's sums stay in fp32: as below, 16 CG columns at a time
+                float *to = a.partial + (((int64_t)r.slice * a.experts + r.e) * a.m + m0 + q * 32) * a.n;
+                constexpr int FP = 4 * CG;               // pieces of 16 bytes of a lane's row
                 for (int c0 = cbeg; c0 < cend; c0 += 32) {
                     uint32_t v[32];
                     __syncwarp();
@@ -796,14 +798,24 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
                         tmem_wait_ld();
                         reg_fence(v);
                     }
-                    float *to = a.partial + (((int64_t)r.slice * a.experts + r.e) * a.m + m0 + rr) * a.n +
-                                r.n0 + c0;
 #pragma unroll
-                    for (int u = 0; u < 32; u += 4)
-                        if (lane < rows && r.n0 + c0 + u < a.n)
-                            *reinterpret_cast<uint4 *>(to + u) =
+                    for (int h = 0; h < 32; h += 4 * FP) {
+#pragma unroll
+                        for (int u = 0; u < FP; ++u)
+                            *staged<FP>(stage, lane, u) =
                                 none ? make_uint4(0u, 0u, 0u, 0u)
-                                     : make_uint4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+                                     : make_uint4(v[h + 4 * u], v[h + 4 * u + 1], v[h + 4 * u + 2], v[h + 4 * u + 3]);
+                        __syncwarp();
+                        const int col = r.n0 + c0 + h + 4 * (lane % FP);
+#pragma unroll
+                        for (int u = 0; u < FP; ++u) {
+                            const int row = u * (32 / FP) + lane / FP;
+                            const uint4 x = *staged<FP>(stage, row, lane % FP);
+                            if (row < rows && col < a.n)
+                                *reinterpret_cast<uint4 *>(to + (int64_t)row * a.n + col) = x;
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             // the product itself first, where it is wanted, then what becomes of it
@@ -880,23 +892,21 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
     }
 }
 
-// out = the slices' sums added up in order, 8 elements per thread.
-__global__ void __launch_bounds__(256) sum_slices_kernel(const float *__restrict__ partial, int slices,
+// out = the slices' sums added up in order, 4 elements per thread.
+__global__ void __launch_bounds__(128) sum_slices_kernel(const float *__restrict__ partial, int slices,
                                                          int64_t n, __nv_bfloat16 *__restrict__ out)
 {
     grid_dep_wait();
     grid_dep_release();
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int64_t i = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 4;
     if (i >= n) return;
-    float f[8] = {};
-#pragma unroll 8
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
     for (int s = 0; s < slices; ++s) {
-        const float4 a = reinterpret_cast<const float4 *>(partial + s * n + i)[0];
-        const float4 b = reinterpret_cast<const float4 *>(partial + s * n + i)[1];
-        f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
-        f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+        const float4 a = *reinterpret_cast<const float4 *>(partial + s * n + i);
+        f.x += a.x; f.y += a.y; f.z += a.z; f.w += a.w;
     }
-    *reinterpret_cast<uint4 *>(out + i) = pack8(f);
+    *reinterpret_cast<uint2 *>(out + i) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
@@ -1064,7 +1074,9 @@ static int64_t dw_tiles(int cg, int experts, int k, int n)
 }
 
 // Few tiles and many rows: the experts' rows are cut so that the device has work for its SMs, but
-// to no less than 256 rows on average.  The slices' fp32 sums are at most 148 tiles of 64 KB.
+// to no less than 256 rows on average.  The slices' fp32 sums are at most 148 tiles of 64 KB.  16384
+// rows over experts of 512 x 512, whole against parts by single CTAs against parts by pairs: two
+// experts 72, 26 and 23 us; four 51, 31 and 25; one of 32768 rows 189, 33 and 31.
 DwPlan expert_dw_plan(int64_t rows, int experts, int k, int n)
 {
     constexpr int64_t kSms = 148;            // (the workspace's size must not depend on the device)
@@ -1098,7 +1110,7 @@ cudaError_t launch_expert_proj_dw(const ProjArgs &p, cudaStream_t st)
     const int64_t tiles = a.slices * dw_tiles(plan.pair ? 2 : 1, p.experts, p.k, p.n);
     cudaError_t e = plan.pair ? run_egemm<P_DW, 2>(a, tiles, st) : run_egemm<P_DW, 1>(a, tiles, st);
     if (e != cudaSuccess || a.slices == 1) return e;
-    return launch_pdl(sum_slices_kernel, dim3((unsigned)((all / 8 + 255) / 256)), dim3(256), 0, st,
+    return launch_pdl(sum_slices_kernel, dim3((unsigned)((all / 4 + 127) / 128)), dim3(128), 0, st,
                       (const float *)p.partial, a.slices, all, a.out);
 }
 
