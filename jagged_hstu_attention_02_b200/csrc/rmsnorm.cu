@@ -60,10 +60,23 @@ __device__ __forceinline__ float scale_top(float m)
     return m > 0.f ? fmaxf(m, 7.888609e-31f /* 2^-100 */) : 0.f;
 }
 
-// 448 / m to 2 ulp (m is 0 or in the range of normal numbers).
+// 448 / m to 2 ulp (m is 0 or in the range of normal numbers).  Of 451 M values 302 come out one e4m3
+// step from those of exact arithmetic, 362 with every operation rounded to nearest; a step of Newton's
+// here makes that 261 and 16384 x 4096 bf16 3 % slower.
 __device__ __forceinline__ float scale_back(float m)
 {
     return m > 0.f ? __fdividef(kE4m3Max, m) : 0.f;
+}
+
+// rs as a power of two times a factor in [1, 2).  The 8-bit values do not depend on the factor: it
+// goes into the scales alone, and the values carry one rounding less.
+__device__ __forceinline__ float power_of(float rs)
+{
+    return isnan(rs) ? rs : __uint_as_float(__float_as_uint(rs) & 0x7f800000u);
+}
+__device__ __forceinline__ float factor_of(float rs)
+{
+    return __uint_as_float((__float_as_uint(rs) & 0x007fffffu) | 0x3f800000u);
 }
 
 template <int W>
@@ -171,7 +184,7 @@ __device__ __forceinline__ void store8_e4m3(uint8_t *row, int c0, int width, con
 // y * (448 / max) and the scales of one chunk of 256 columns from c0, in groups of `group`
 // columns (32, 64 or 128): group / 8 neighbouring lanes.
 __device__ __forceinline__ void scale_groups(float (&h)[8], int c0, int width, int group,
-                                             float *scales)
+                                             float factor, float *scales)
 {
     float m = 0.f;
 #pragma unroll
@@ -179,7 +192,7 @@ __device__ __forceinline__ void scale_groups(float (&h)[8], int c0, int width, i
     for (int o = group / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
     m = scale_top(m);
     const int i = elem8(c0), shift = 31 - __clz(group);    // a power of two
-    if (i < width && (i & (group - 1)) == 0) scales[i >> shift] = m * (1.f / kE4m3Max);
+    if (i < width && (i & (group - 1)) == 0) scales[i >> shift] = m * factor * (1.f / kE4m3Max);
     const float back = scale_back(m);
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] *= back;
@@ -190,7 +203,7 @@ __device__ __forceinline__ void scale_groups(float (&h)[8], int c0, int width, i
 // the order of maxima does not matter).
 template <int W, int NC>
 __device__ __forceinline__ void scale_groups_shifted(float (&h)[NC][8], int skew, int width, int group,
-                                                     float *scales, uint32_t *gm)
+                                                     float factor, float *scales, uint32_t *gm)
 {
     const int t = threadIdx.x % (32 * W), wg = (threadIdx.x / 32) % W;
     const int shift = 31 - __clz(group), groups = (width + group - 1) / group;
@@ -213,7 +226,7 @@ __device__ __forceinline__ void scale_groups_shifted(float (&h)[NC][8], int skew
     }
     group_sync<W>();
     for (int g = t; g < groups; g += 32 * W)
-        scales[g] = scale_top(__uint_as_float(gm[g])) * (1.f / kE4m3Max);
+        scales[g] = scale_top(__uint_as_float(gm[g])) * factor * (1.f / kE4m3Max);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = elem8((c * W + wg) * 256 - skew);
@@ -314,6 +327,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
             }
         }
         const float rs = landed ? rsqrtf(ss / (float)width + a.eps) : CUDART_NAN_F;
+        const float power = power_of(rs), factor = factor_of(rs);      // (8 bits only)
         if (a.rstd && lead) a.rstd[row] = rs;
         if (a.sum) {
 #pragma unroll
@@ -323,7 +337,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[c][e] *= rs * w[c][e];
+            for (int e = 0; e < 8; ++e) h[c][e] *= (E4M3 ? power : rs) * w[c][e];
         if constexpr (!E4M3) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -337,7 +351,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
 #pragma unroll
                     for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[c][e]));
                 m = scale_top(group_reduce<W, true>(m, buf[1]));
-                if (lead) a.scales[row] = m * (1.f / kE4m3Max);
+                if (lead) a.scales[row] = m * factor * (1.f / kE4m3Max);
                 const float back = scale_back(m);
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
@@ -345,13 +359,14 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
                     for (int e = 0; e < 8; ++e) h[c][e] *= back;
             } else if constexpr (!VEC) {
                 const int groups = (width + a.group - 1) / a.group;
-                scale_groups_shifted<W, NC>(h, skew, width, a.group, a.scales + row * groups,
+                scale_groups_shifted<W, NC>(h, skew, width, a.group, factor, a.scales + row * groups,
                                             reinterpret_cast<uint32_t *>(smem) + group * groups);
             } else {
                 const int groups = (width + a.group - 1) / a.group;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    scale_groups(h[c], (c * W + wg) * 256, width, a.group, a.scales + row * groups);
+                    scale_groups(h[c], (c * W + wg) * 256, width, a.group, factor,
+                                 a.scales + row * groups);
                 if constexpr (W > 1) group_sync<W>();
             }
 #pragma unroll
