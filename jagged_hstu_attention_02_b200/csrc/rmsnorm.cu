@@ -550,7 +550,7 @@ int warps_for(int width)
 }
 
 // How many blocks share an SM and how deep their rings are: rows in flight of `flight` bytes per
-// SM.  (Forward, 64 KB: 16384 x 4096 bf16 to e4m3 takes 75 us; with 128 KB in flight 82 and with
+// SM.  (Forward, 64 KB: 16384 x 4096 bf16 to e4m3 takes 79 us; with 128 KB in flight 82 and with
 // 192 KB 88, as reads that run further ahead only crowd the writes; with half the warps 91.)
 // The blocks' shared memory is sized to leave no room for more of them, or a kernel behind
 // this one would place its blocks unevenly.
