@@ -10,7 +10,9 @@
 // thread 2 chunks of 8 elements, kept in registers between the sum of squares and the output.
 // A group's chain per row (load, sum, scale, store) is all latency, so with more rows than
 // groups the groups stay and their rows arrive ahead of them through a ring of bulk copies in
-// shared memory (RING); with fewer, or where rows do not start on 16 bytes, they load directly.
+// shared memory (RING); with fewer they load directly.  Rows that start anywhere come with the rest
+// of their first and last 16 bytes (SHIFTED_RING; 16384 x 1001 bf16, against direct loads: forward
+// 41.7 -> 31.0 us, to e4m3 59.3 -> 47.4, backward 71.6 -> 38.1).
 // The forward normalises the fp32 sum, before it is rounded to the stored h.
 #include <cuda_fp8.h>
 #include <math_constants.h>
@@ -36,12 +38,14 @@ using sm100::smem_u32;
 constexpr int kMaxRing = 4;
 constexpr float kE4m3Max = 448.f;
 
-// How rows are read: through the ring, directly, or directly where they start anywhere.
-enum Access { RING, DIRECT, SHIFTED };
+// How rows are read: through the ring or directly, rows that start on 16 bytes or anywhere.
+enum Access { RING, DIRECT, SHIFTED_RING, SHIFTED };
+constexpr bool on_pieces(Access a) { return a == RING || a == DIRECT; }
+constexpr bool staged_rows(Access a) { return a == RING || a == SHIFTED_RING; }
 
 // Chunks of 8 elements per thread.  Rows that start anywhere need up to 7 elements more.
 template <int W, Access A>
-constexpr int chunks() { return A == SHIFTED && W == 32 ? 3 : 2; }
+constexpr int chunks() { return !on_pieces(A) && W == 32 ? 3 : 2; }
 
 template <int W> struct NormShape {
     static constexpr int kGroups = W < 8 ? 8 / W : 1;      // per block
@@ -124,21 +128,78 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void ring_fill(const Ring &r, int stage, const uint8_t *const (&in)[N],
-                                          int64_t row, uint32_t row_bytes)
+// Bytes that a row takes in a stage.  A row that starts anywhere keeps the up to 7 elements in front
+// of it that share its first piece, so its pieces are on 16 bytes there too.
+template <Access A, typename T>
+__host__ __device__ constexpr int row_slot(int width)
 {
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int n = 0; n < N; ++n) bytes += in[n] ? row_bytes : 0;
-    mbar_arrive_expect_tx(&r.full[stage], bytes);
+    return (on_pieces(A) ? width : (width + 14) / 8 * 8) * (int)sizeof(T);
+}
+
+// Copies row `row` of each tensor of `in` to the stage, from `skew` elements in front of it and to
+// the end of its last 16 bytes; where the tensor ends before that, its last elements one by one.
+template <Access A, typename T, int N>
+__device__ __forceinline__ void ring_fill(const Ring &r, int stage, const T *const (&in)[N], int64_t row,
+                                          int width, int skew, int64_t rows)
+{
     uint8_t *dst = r.base + stage * r.stage_bytes;
+    const uint32_t slot = (uint32_t)row_slot<A, T>(width);
+    uint32_t bytes = slot, all = 0;
+    const T *src[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) src[n] = in[n] ? in[n] + row * width - skew : nullptr;
+    if constexpr (!on_pieces(A)) {
+        const uint32_t need = (uint32_t)(skew + width) * sizeof(T);
+        bytes = (need + 15) & ~15u;
+        if (((rows - row) * width + skew) * (int64_t)sizeof(T) < bytes) {
+            bytes = need & ~15u;
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                for (uint32_t i = bytes / sizeof(T); src[n] && i < need / sizeof(T); ++i)
+                    reinterpret_cast<T *>(dst + n * slot)[i] = src[n][i];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) all += in[n] ? bytes : 0u;
+    mbar_arrive_expect_tx(&r.full[stage], all);
 #pragma unroll
     for (int n = 0; n < N; ++n)
         if (in[n]) {
-            bulk_load(dst, in[n] + row * row_bytes, row_bytes, &r.full[stage]);
-            dst += row_bytes;
+            if (on_pieces(A) || bytes) bulk_load(dst, src[n], bytes, &r.full[stage]);
+            dst += slot;
         }
+}
+
+// A lane's 8 elements of a staged row that starts anywhere; zeros outside the row.
+template <typename T>
+__device__ __forceinline__ void load8_staged(const T *row, int c0, int width, float (&f)[8])
+{
+    const int i = elem8(c0);
+    uint4 v[sizeof(T) / 2] = {};
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+        if (i + 8 > 0 && i < width) v[k] = reinterpret_cast<const uint4 *>(row + i)[k];
+    if constexpr (sizeof(T) == 2) {
+        unpack8(v[0], f);
+    } else {
+        f[0] = __uint_as_float(v[0].x); f[1] = __uint_as_float(v[0].y);
+        f[2] = __uint_as_float(v[0].z); f[3] = __uint_as_float(v[0].w);
+        f[4] = __uint_as_float(v[1].x); f[5] = __uint_as_float(v[1].y);
+        f[6] = __uint_as_float(v[1].z); f[7] = __uint_as_float(v[1].w);
+    }
+    if (c0 >= 0 && c0 + 256 <= width) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (i + e < 0 || i + e >= width) f[e] = 0.f;
+}
+
+// 8 elements of a row as A reads it: `row` in a stage or in the tensor [begin, end).
+template <Access A, typename T>
+__device__ __forceinline__ void read8(const T *row, int c0, int width, const T *begin, const T *end,
+                                      float (&f)[8])
+{
+    if constexpr (A == SHIFTED_RING) load8_staged(row, c0, width, f);
+    else load8<on_pieces(A)>(row, c0, width, begin, end, f);
 }
 
 // Waits for a stage; false if its copies have not landed within the limit (of a sound device
@@ -241,11 +302,11 @@ __device__ __forceinline__ void scale_groups_shifted(float (&h)[NC][8], int skew
 
 template <typename T, int W, bool E4M3, Access A>
 __global__ void __launch_bounds__(NormShape<W>::kThreads,
-                                  A == SHIFTED ? NormShape<W>::shifted_blocks(E4M3)
-                                               : NormShape<W>::kFwdBlocks)
+                                  on_pieces(A) ? NormShape<W>::kFwdBlocks
+                                               : NormShape<W>::shifted_blocks(E4M3))
     rms_norm_kernel(const __grid_constant__ RmsArgs a, int depth)
 {
-    constexpr bool VEC = A != SHIFTED;
+    constexpr bool VEC = on_pieces(A), STAGED = staged_rows(A);
     constexpr int NC = chunks<W, A>();
     constexpr int kGroups = NormShape<W>::kGroups;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -257,12 +318,10 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
     const int width = a.width;
     // the same for all rows of a group: the stride is a multiple of 8 (or there is one row)
     const int skew = lead_of<VEC>(row, width);
-    const uint32_t row_bytes = (uint32_t)width * sizeof(T);
-    const uint8_t *const in[2] = {reinterpret_cast<const uint8_t *>(a.x),
-                                  reinterpret_cast<const uint8_t *>(a.resid)};
+    const T *const in[2] = {reinterpret_cast<const T *>(a.x), reinterpret_cast<const T *>(a.resid)};
     Ring ring;
-    if constexpr (A == RING) {
-        ring = ring_of<W>(smem, depth, (a.resid ? 2 : 1) * row_bytes);
+    if constexpr (STAGED) {
+        ring = ring_of<W>(smem, depth, (a.resid ? 2 : 1) * row_slot<A, T>(width));
         if (lead) {
             for (int s = 0; s < depth; ++s) mbar_init(&ring.full[s], 1);
             sm100::fence_mbar_init();
@@ -271,9 +330,9 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
     }
     grid_dep_wait();
     grid_dep_release();
-    if (A == RING && lead)
+    if (STAGED && lead)
         for (int s = 0; s < depth && row + s * stride < a.rows; ++s)
-            ring_fill(ring, s, in, row + s * stride, row_bytes);
+            ring_fill<A>(ring, s, in, row + s * stride, width, skew, a.rows);
     float w[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -293,19 +352,19 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
         const T *x = reinterpret_cast<const T *>(a.x) + base;
         const T *r = a.resid ? reinterpret_cast<const T *>(a.resid) + base : nullptr;
         bool landed = true;
-        if constexpr (A == RING) {
+        if constexpr (STAGED) {
             landed = ring_wait(ring, stage, parity);
-            x = reinterpret_cast<const T *>(ring.base + stage * ring.stage_bytes);
-            r = a.resid ? x + width : nullptr;
+            x = reinterpret_cast<const T *>(ring.base + stage * ring.stage_bytes) + skew;
+            r = a.resid ? x + row_slot<A, T>(width) / sizeof(T) : nullptr;
         }
         float h[NC][8];
         float ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load8<VEC>(x, (c * W + wg) * 256 - skew, width, x_begin, x_end, h[c]);
+        for (int c = 0; c < NC; ++c) read8<A>(x, (c * W + wg) * 256 - skew, width, x_begin, x_end, h[c]);
         if (r) {
             float b[NC][8];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) load8<VEC>(r, (c * W + wg) * 256 - skew, width, r_begin, r_end, b[c]);
+            for (int c = 0; c < NC; ++c) read8<A>(r, (c * W + wg) * 256 - skew, width, r_begin, r_end, b[c]);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -316,11 +375,11 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
         ss = group_reduce<W, false>(ss, buf[0]);
-        if constexpr (A == RING) {
+        if constexpr (STAGED) {
             // every thread of the group has read the stage
             if constexpr (W == 1) __syncwarp();
             if (lead && row + depth * stride < a.rows)
-                ring_fill(ring, stage, in, row + depth * stride, row_bytes);
+                ring_fill<A>(ring, stage, in, row + depth * stride, width, skew, a.rows);
             if (++stage == depth) {
                 stage = 0;
                 parity ^= 1;
@@ -359,8 +418,11 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads,
                     for (int e = 0; e < 8; ++e) h[c][e] *= back;
             } else if constexpr (!VEC) {
                 const int groups = (width + a.group - 1) / a.group;
+                uint32_t *maxima = reinterpret_cast<uint32_t *>(smem);
+                if constexpr (STAGED)                      // behind the stages of all groups
+                    maxima += kGroups * (kMaxRing * 8 + depth * ring.stage_bytes) / 4;
                 scale_groups_shifted<W, NC>(h, skew, width, a.group, factor, a.scales + row * groups,
-                                            reinterpret_cast<uint32_t *>(smem) + group * groups);
+                                            maxima + group * groups);
             } else {
                 const int groups = (width + a.group - 1) / a.group;
 #pragma unroll
@@ -383,7 +445,7 @@ template <typename T, int W, Access A>
 __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBlocks)
     rms_norm_bwd_kernel(const __grid_constant__ RmsBwdArgs a, int depth)
 {
-    constexpr bool VEC = A != SHIFTED;
+    constexpr bool VEC = on_pieces(A), STAGED = staged_rows(A);
     constexpr int NC = chunks<W, A>();
     constexpr int kGroups = NormShape<W>::kGroups;
     extern __shared__ __align__(128) uint8_t smem[];       // the ring, then [kGroups][width] floats
@@ -394,13 +456,11 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
     int64_t row = (int64_t)blockIdx.x * kGroups + group;
     const int width = a.width;
     const int skew = lead_of<VEC>(row, width);             // of all rows of the group
-    const uint32_t row_bytes = (uint32_t)width * sizeof(T);
-    const uint8_t *const in[3] = {reinterpret_cast<const uint8_t *>(a.dy),
-                                  reinterpret_cast<const uint8_t *>(a.h),
-                                  reinterpret_cast<const uint8_t *>(a.dsum)};
+    const T *const in[3] = {reinterpret_cast<const T *>(a.dy), reinterpret_cast<const T *>(a.h),
+                            reinterpret_cast<const T *>(a.dsum)};
     Ring ring;
-    if constexpr (A == RING) {
-        ring = ring_of<W>(smem, depth, (a.dsum ? 3 : 2) * row_bytes);
+    if constexpr (STAGED) {
+        ring = ring_of<W>(smem, depth, (a.dsum ? 3 : 2) * row_slot<A, T>(width));
         if (lead) {
             for (int s = 0; s < depth; ++s) mbar_init(&ring.full[s], 1);
             sm100::fence_mbar_init();
@@ -409,9 +469,9 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
     }
     grid_dep_wait();
     grid_dep_release();
-    if (A == RING && lead)
+    if (STAGED && lead)
         for (int s = 0; s < depth && row + s * stride < a.rows; ++s)
-            ring_fill(ring, s, in, row + s * stride, row_bytes);
+            ring_fill<A>(ring, s, in, row + s * stride, width, skew, a.rows);
     // the weights stay in registers: with shared memory full of rows L1 keeps nothing, and
     // reading them again for every row took 127 us instead of 83 (8192 x 8192 bf16)
     float acc[NC][8], w[NC][8];
@@ -437,18 +497,18 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
         const T *ds = a.dsum ? reinterpret_cast<const T *>(a.dsum) + base : nullptr;
         float rs = rs_next;
         if (row + stride < a.rows) rs_next = a.rstd[row + stride];
-        if constexpr (A == RING) {
+        if constexpr (STAGED) {
             if (!ring_wait(ring, stage, parity)) rs = CUDART_NAN_F;
-            dy = reinterpret_cast<const T *>(ring.base + stage * ring.stage_bytes);
-            hp = dy + width;
-            ds = a.dsum ? hp + width : nullptr;
+            dy = reinterpret_cast<const T *>(ring.base + stage * ring.stage_bytes) + skew;
+            hp = dy + row_slot<A, T>(width) / sizeof(T);
+            ds = a.dsum ? hp + row_slot<A, T>(width) / sizeof(T) : nullptr;
         }
         float g[NC][8], h[NC][8];
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            load8<VEC>(dy, (c * W + wg) * 256 - skew, width, dy_begin, dy_end, g[c]);
-            load8<VEC>(hp, (c * W + wg) * 256 - skew, width, h_begin, h_end, h[c]);
+            read8<A>(dy, (c * W + wg) * 256 - skew, width, dy_begin, dy_end, g[c]);
+            read8<A>(hp, (c * W + wg) * 256 - skew, width, h_begin, h_end, h[c]);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -464,7 +524,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float o[8];
-            if (ds) load8<VEC>(ds, (c * W + wg) * 256 - skew, width, ds_begin, ds_end, o);
+            if (ds) read8<A>(ds, (c * W + wg) * 256 - skew, width, ds_begin, ds_end, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float d = rs * (g[c][e] - h[c][e] * dot);
@@ -472,10 +532,10 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
             }
             store8<VEC>(dx, (c * W + wg) * 256 - skew, width, o);
         }
-        if constexpr (A == RING) {
+        if constexpr (STAGED) {
             group_sync<W>();                               // the group has read the stage
             if (lead && row + depth * stride < a.rows)
-                ring_fill(ring, stage, in, row + depth * stride, row_bytes);
+                ring_fill<A>(ring, stage, in, row + depth * stride, width, skew, a.rows);
             if (++stage == depth) {
                 stage = 0;
                 parity ^= 1;
@@ -560,16 +620,16 @@ struct RingPlan {
 };
 
 template <int W>
-RingPlan ring_plan(int blocks, int64_t stage_bytes, int64_t flight)
+RingPlan ring_plan(int blocks, int64_t stage_bytes, int64_t flight, int64_t extra = 0)
 {
     constexpr int64_t kSmem = 227 * 1024, kGroups = NormShape<W>::kGroups;
     RingPlan p;
     p.blocks = blocks;
     while (p.blocks > 1 && p.blocks * kGroups * stage_bytes > flight) p.blocks /= 2;
-    const int64_t room = kSmem / p.blocks - 2048;
+    const int64_t room = kSmem / p.blocks - 2048 - extra;
     const int64_t most = std::min<int64_t>(kMaxRing, (room - kGroups * kMaxRing * 8) / (kGroups * stage_bytes));
     p.depth = (int)std::max<int64_t>(1, std::min(most, flight / (p.blocks * kGroups * stage_bytes)));
-    p.smem = (size_t)room;
+    p.smem = (size_t)(room + extra);
     return p;
 }
 
@@ -591,8 +651,12 @@ cudaError_t run_fwd(const RmsArgs &a, cudaStream_t st)
         // groups keep their rows' alignment: a stride of a multiple of 8 rows
         const int64_t stay = (int64_t)num_sms() * S::shifted_blocks(E4M3) / 8 * 8;
         const size_t maxima = E4M3 && a.group ? (size_t)S::kGroups * ((a.width + a.group - 1) / a.group) * 4 : 0;
-        return launch_norm<rms_norm_kernel<T, W, E4M3, SHIFTED>>(a, std::min(blocks, stay),
-                           S::kThreads, maxima, 0, st);
+        if (blocks <= stay)
+            return launch_norm<rms_norm_kernel<T, W, E4M3, SHIFTED>>(a, blocks, S::kThreads, maxima, 0, st);
+        const int64_t stage = (int64_t)row_slot<SHIFTED_RING, T>(a.width) * (a.resid ? 2 : 1);
+        const RingPlan p = ring_plan<W>(S::shifted_blocks(E4M3), stage, 64 * 1024, (int64_t)maxima);
+        return launch_norm<rms_norm_kernel<T, W, E4M3, SHIFTED_RING>>(
+            a, (int64_t)num_sms() * p.blocks / 8 * 8, S::kThreads, p.smem, p.depth, st);
     }
     if (blocks <= most)
         return launch_norm<rms_norm_kernel<T, W, E4M3, DIRECT>>(a, blocks, S::kThreads, 0, 0, st);
@@ -622,10 +686,13 @@ cudaError_t run_bwd(const RmsBwdArgs &a, cudaStream_t st)
     const int blocks = rms_bwd_blocks(a.rows, a.width);
     const size_t parts = S::kGroups > 1 && a.dweight ? (size_t)S::kGroups * a.width * 4 : 0;
     cudaError_t e;
-    if (a.width % 8 != 0) {
-        e = launch_norm<rms_norm_bwd_kernel<T, W, SHIFTED>>(a, blocks, S::kThreads, parts, 0, st);
-    } else if (a.rows <= (int64_t)blocks * S::kGroups) {
-        e = launch_norm<rms_norm_bwd_kernel<T, W, DIRECT>>(a, blocks, S::kThreads, parts, 0, st);
+    if (a.rows <= (int64_t)blocks * S::kGroups) {
+        e = a.width % 8 != 0 ? launch_norm<rms_norm_bwd_kernel<T, W, SHIFTED>>(a, blocks, S::kThreads, parts, 0, st)
+                             : launch_norm<rms_norm_bwd_kernel<T, W, DIRECT>>(a, blocks, S::kThreads, parts, 0, st);
+    } else if (a.width % 8 != 0) {
+        const int64_t stage = (int64_t)row_slot<SHIFTED_RING, T>(a.width) * (a.dsum ? 3 : 2);
+        const RingPlan p = ring_plan<W>(S::kBwdBlocks, stage, 160 * 1024);
+        e = launch_norm<rms_norm_bwd_kernel<T, W, SHIFTED_RING>>(a, blocks, S::kThreads, p.smem, p.depth, st);
     } else {
         const int64_t stage = (int64_t)a.width * sizeof(T) * (a.dsum ? 3 : 2);
         const RingPlan p = ring_plan<W>(S::kBwdBlocks, stage, 160 * 1024);

@@ -203,6 +203,48 @@ def test_norm_bwd_parts_left_out_and_in_place():
     assert not dw.any()
 
 
+# more rows than groups of warps, rows that start anywhere: they arrive through the ring
+MANY_ROWS = [(20001, 1), (9001, 7), (5003, 33), (5000, 499), (2999, 1001), (1501, 2001), (700, 4085),
+             (333, 8001), (301, 16383)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", MANY_ROWS)
+def test_norm_of_many_rows_that_start_anywhere(shape, dtype):
+    test_norm(shape, True, True, dtype)
+    test_norm(shape, False, False, dtype)
+    test_norm_e4m3(shape, 0, dtype)
+    test_norm_e4m3(shape, 32, dtype)
+    test_norm_bwd(shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(9001, 7), (5003, 33), (2999, 1001), (301, 16383)])
+def test_norm_rows_do_not_see_their_neighbours(shape, dtype):
+    x, r, w = _norm_inputs(*shape, dtype, 5)
+    clean = ops.rms_norm_rows(x, w, r, training=True)
+    q = ops.rms_norm_rows(x, w, r, e4m3=True, group=64)
+    dirty = x.clone()
+    dirty[::2] = float("nan")
+    d = ops.rms_norm_rows(dirty, w, r, training=True)
+    dq = ops.rms_norm_rows(dirty, w, r, e4m3=True, group=64)
+    for a, b in ((clean.y, d.y), (clean.sum, d.sum), (clean.rstd, d.rstd), (q.y, dq.y), (q.scales, dq.scales)):
+        a, b = a[1::2].contiguous(), b[1::2].contiguous()
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.isnan(d.y[::2].float()).all()
+    # gradients, and results written over inputs
+    dx, _ = ops.rms_norm_rows_bwd(r, clean.sum, clean.rstd, w, dsum=x)
+    ddx, _ = ops.rms_norm_rows_bwd(r, clean.sum, clean.rstd, w, dsum=dirty)
+    assert torch.equal(dx[1::2], ddx[1::2])
+    over = r.clone()
+    y = torch.empty_like(x)
+    ops.rms_norm_rows(x, w, over, out=ops.RmsNorm(y, None, over, None))
+    assert torch.equal(y, clean.y) and torch.equal(over, clean.sum)
+    over = x.clone()
+    ops.rms_norm_rows_bwd(r, clean.sum, clean.rstd, w, dsum=over, grads=(over, torch.empty_like(w)))
+    assert torch.equal(over, dx)
+
+
 # ------------------------------------------------------------------ routing
 
 def _ids(rng, T, k, E, bad=0.1, dtype=np.int32):
