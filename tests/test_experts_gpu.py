@@ -560,6 +560,30 @@ def test_weight_gradients_from_parts_of_the_rows(counts, K, N):
     assert torch.equal(again, gw.t)
 
 
+# few tiles and long contractions: several blocks share a tile, each a part of the contraction
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 130], [64, 65], [128, 7, 1, 0, 127], [2] * 7], ids=str)
+@pytest.mark.parametrize("K,N", [(1024, 64), (2048, 136), (520, 264), (1032, 72), (4104, 8), (264, 128)])
+def test_products_whose_contraction_is_shared(counts, K, N):
+    test_proj(counts, K, N)
+    test_proj_e4m3(counts, -(-K // 16) * 16, N)
+    test_proj_bwd(counts, N, K)
+
+
+def test_shared_contractions_repeat_and_cover_overlapping_experts():
+    x, w, _, S, _ = _proj_case([4990, 0, 0, 10], 512, 64, 0, 8)
+    off = torch.tensor([0, 4990, 0, 4990, 5000], dtype=torch.int64, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = ops.expert_proj(x, w, off, status=status)
+    assert status.item() == ops.DEV_BAD_OFFSETS              # expert 1 ends ahead of its start
+    ref = ox.proj(_np(x[4990:]), _np(w[3:]), np.array([0, 10]))
+    size = ox.proj(np.abs(_np(x[4990:])), np.abs(_np(w[3:])), np.array([0, 10]))
+    _close(out[4990:], ref, np.abs(ref) * 2 ** -8 + _dot_tol(512, size), "behind the overlap")
+    x, w, off, S, E = _proj_case([64, 65], 4104, 136, 0, 9)
+    first = ops.expert_proj(x, w, off, silu=True)
+    for _ in range(5):
+        assert torch.equal(ops.expert_proj(x, w, off, silu=True), first)
+
+
 def test_proj_without_rows():
     x, w, off, _, _ = _proj_case([0, 0], 64, 64, 0, 1)
     assert ops.expert_proj(x, w, off).shape == (0, 64)
@@ -629,8 +653,11 @@ def test_tensors_of_more_than_two_to_the_31_elements():
     w = _rand(2, E, W, 64, scale=W ** -0.5)
     off = torch.tensor([0, S - 1, S], device="cuda")
     y = ops.expert_proj(x, w, off)
-    tiny = ops.expert_proj(part, w, torch.tensor([0, 3, 4], device="cuda"))
-    assert torch.equal(y[ends], tiny)
+    # (each on its own: few rows share the contraction among blocks, so the sums' order differs)
+    few = np.array([0, 3, 4])
+    ref, size = ox.proj(_np(part), _np(w), few), ox.proj(np.abs(_np(part)), np.abs(_np(w)), few)
+    for got in (y[ends], ops.expert_proj(part, w, torch.from_numpy(few).cuda())):
+        _close(got, ref, np.abs(ref) * 2 ** -8 + _dot_tol(W, size), "ends")
     xs = ops.expert_dispatch(part[:2], slots, out=x)
     assert torch.equal(xs[ends], torch.stack([part[0], part[1], part[1], part[0]]))
 
