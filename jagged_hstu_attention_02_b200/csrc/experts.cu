@@ -302,8 +302,9 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 }
 
 // The same for rows that start anywhere (row_bytes no multiple of 16), 512 bytes per warp and
-// turn, the token's row put together for each of its places as that place lies; ES: the bytes
-// that a row's ends are cut to.
+// turn.  A lane keeps an aligned piece of the token's row and its two neighbours; where each place
+// lies decides which two of them hold an aligned piece there, and by how much they shift.  ES: the
+// bytes that a row's ends are cut to.
 template <int ES>
 __global__ void __launch_bounds__(32 * kRowWarps)
     expert_dispatch_shifted_kernel(const __grid_constant__ DispatchArgs a, int wpr)
@@ -317,15 +318,32 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     int mine = lane < a.choices ? a.slots[t * a.choices + lane] : -1;
     if (mine >= a.max_rows) mine = -1;
     const uint8_t *src = a.x + t * a.row_bytes, *end = a.x + a.tokens * a.row_bytes;
-    for (int j = 0; j < a.choices; ++j) {
-        const int s = __shfl_sync(kFullMask, mine, j);
-        if (s < 0) continue;
-        uint8_t *dst = a.out + (int64_t)s * a.row_bytes;
-        const int lead = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
-        for (int64_t c0 = part * 512 - lead; c0 < a.row_bytes; c0 += 512 * wpr) {
-            uint32_t v[4];
-            load_words<4>(src + c0, src, src + a.row_bytes, a.x, end, v);
-            store_words<4, ES>(dst + c0, dst, dst + a.row_bytes, v);
+    const int from = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+    // (places lie up to 15 bytes in front of their pieces' row, so the last piece may be one further)
+    for (int64_t c0 = part * 512; c0 < a.row_bytes + 15; c0 += 512 * wpr) {
+        const uint8_t *at = src - from + c0;
+        uint32_t x[12] = {}, edge[4] = {};               // the pieces before, at and behind `at`
+        load_piece(at + 16 * lane, a.x, end, x + 4);
+        if (lane == 0 || lane == 31) load_piece(lane ? at + 512 : at - 16, a.x, end, edge);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = __shfl_up_sync(kFullMask, x[4 + i], 1);
+            const uint32_t d = __shfl_down_sync(kFullMask, x[4 + i], 1);
+            x[i] = lane ? u : edge[i];
+            x[8 + i] = lane < 31 ? d : edge[i];
+        }
+        for (int j = 0; j < a.choices; ++j) {
+            const int s = __shfl_sync(kFullMask, mine, j);
+            if (s < 0) continue;
+            uint8_t *dst = a.out + (int64_t)s * a.row_bytes, *to = dst + a.row_bytes;
+            const int lead = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = from < lead ? x[i] : x[4 + i];
+            shift_words<8, 2>(v, (from - lead) & 15);
+            uint8_t *p = dst - lead + c0 + 16 * lane;
+            if (p >= dst && p + 16 <= to) *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+            else if (p + 16 > dst && p < to) store_cut<4, ES>(p, v, dst, to);
         }
     }
     if (part != 0 || !a.scales) return;
