@@ -259,6 +259,39 @@ int warps_per_row(int64_t pieces, int per_lane)
     return w;
 }
 
+constexpr int kLaneElems = 4;
+
+// An element as it lies in memory, if `yes`, else 0.  (Inline for the reason at load16_if.)
+__device__ __forceinline__ void load_elem(const void *p, bool yes, uint16_t &v)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t@q ld.global.b16 %0, [%1];\n\t}"
+                 : "=&h"(v) : "l"(p), "r"((int)yes));
+}
+__device__ __forceinline__ void load_elem(const void *p, bool yes, uint32_t &v)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.b32 %0, [%1];\n\t}"
+                 : "=&r"(v) : "l"(p), "r"((int)yes));
+}
+__device__ __forceinline__ void load_elem(const void *p, bool yes, uint64_t &v)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b64 %0, 0;\n\t@q ld.global.b64 %0, [%1];\n\t}"
+                 : "=&l"(v) : "l"(p), "r"((int)yes));
+}
+__device__ __forceinline__ float elem(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ float elem(uint32_t v) { return __uint_as_float(v); }
+__device__ __forceinline__ void store_elem(__nv_bfloat16 *p, float f) { *p = __float2bfloat16_rn(f); }
+__device__ __forceinline__ void store_elem(float *p, float f) { *p = f; }
+template <typename T> struct ElemBits { using type = uint32_t; };
+template <> struct ElemBits<__nv_bfloat16> { using type = uint16_t; };
+
+// The elements p[0], p[32], ..., `n` of them.
+template <typename T, typename B>
+__device__ __forceinline__ void load_apart(const T *p, int n, B (&v)[kLaneElems])
+{
+#pragma unroll
+    for (int i = 0; i < kLaneElems; ++i) load_elem(p + 32 * i, i < n, v[i]);
+}
+
 // Rows wider than 16 pieces: wpr warps per token read its row once, 4 pieces per lane in
 // flight, and write it to each of the token's places.
 __global__ void __launch_bounds__(32 * kRowWarps)
@@ -301,11 +334,9 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     }
 }
 
-// The same for rows that start anywhere (row_bytes no multiple of 16), 512 bytes per warp and
-// turn.  A lane keeps an aligned piece of the token's row and its two neighbours; where each place
-// lies decides which two of them hold an aligned piece there, and by how much they shift.  ES: the
-// bytes that a row's ends are cut to.
-template <int ES>
+// Rows of an odd number of bytes, 512 bytes per warp and turn.  A lane keeps an aligned piece of the
+// token's row and its two neighbours; where each place lies decides which two of them hold an
+// aligned piece there, and by how much they shift.
 __global__ void __launch_bounds__(32 * kRowWarps)
     expert_dispatch_shifted_kernel(const __grid_constant__ DispatchArgs a, int wpr)
 {
@@ -343,7 +374,49 @@ __global__ void __launch_bounds__(32 * kRowWarps)
             shift_words<8, 2>(v, (from - lead) & 15);
             uint8_t *p = dst - lead + c0 + 16 * lane;
             if (p >= dst && p + 16 <= to) *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
-            else if (p + 16 > dst && p < to) store_cut<4, ES>(p, v, dst, to);
+            else if (p + 16 > dst && p < to) store_cut<4, 1>(p, v, dst, to);
+        }
+    }
+    if (part != 0 || !a.scales) return;
+    for (int j = 0; j < a.choices; ++j) {
+        const int s = __shfl_sync(kFullMask, mine, j);
+        if (s < 0) continue;
+        for (int g = lane; g < a.n_scales; g += 32)
+            a.scales_out[(int64_t)s * a.n_scales + g] = a.scales[t * a.n_scales + g];
+    }
+}
+
+// Rows that start anywhere, of whole elements E (2, 4 or 8 bytes): 128 elements per warp and turn, a
+// lane's 4 lying 32 apart.  One element per access is what all alignments have in common, and a
+// warp's access is still a run of neighbours.  (By shifted pieces, as bytes go, 16384 x 4 places:
+// 1001 bf16 46.4 us against 36.9, 1003 fp32 82 against 57.)
+template <typename E>
+__global__ void __launch_bounds__(32 * kRowWarps)
+    expert_dispatch_apart_kernel(const __grid_constant__ DispatchArgs a, int wpr)
+{
+    grid_dep_wait();
+    grid_dep_release();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (kRowWarps / wpr) + warp / wpr;
+    if (t >= a.tokens) return;
+    const int part = warp % wpr;
+    int mine = lane < a.choices ? a.slots[t * a.choices + lane] : -1;
+    if (mine >= a.max_rows) mine = -1;
+    const int64_t width = a.row_bytes / (int64_t)sizeof(E);
+    const E *src = reinterpret_cast<const E *>(a.x) + t * width;
+    E *out = reinterpret_cast<E *>(a.out);
+    for (int64_t c0 = part * 128; c0 < width; c0 += 128 * wpr) {
+        const int64_t c = c0 + lane;
+        const int n = (int)min((width - c + 31) >> 5, (int64_t)kLaneElems);
+        E v[kLaneElems];
+        load_apart(src + c, n, v);
+        for (int j = 0; j < a.choices; ++j) {
+            const int s = __shfl_sync(kFullMask, mine, j);
+            if (s < 0) continue;
+            E *to = out + s * width + c;
+#pragma unroll
+            for (int i = 0; i < kLaneElems; ++i)
+                if (i < n) to[32 * i] = v[i];
         }
     }
     if (part != 0 || !a.scales) return;
@@ -405,8 +478,11 @@ cudaError_t run_dispatch(const DispatchArgs &a, cudaStream_t st)
     }
     const int wpr = warps_per_row((a.row_bytes + 15) / 16, sizeof(V) == 16 ? 4 : 1);
     const int tokens = kRowWarps / wpr;
-    auto k = sizeof(V) == 16 ? expert_dispatch_kernel
-             : sizeof(V) == 1 ? expert_dispatch_shifted_kernel<1> : expert_dispatch_shifted_kernel<2>;
+    auto k = sizeof(V) == 16  ? expert_dispatch_kernel
+             : sizeof(V) == 8 ? expert_dispatch_apart_kernel<uint64_t>
+             : sizeof(V) == 4 ? expert_dispatch_apart_kernel<uint32_t>
+             : sizeof(V) == 2 ? expert_dispatch_apart_kernel<uint16_t>
+                              : expert_dispatch_shifted_kernel;
     return launch_pdl(k, dim3((unsigned)((a.tokens + tokens - 1) / tokens)), dim3(32 * kRowWarps), 0,
                       st, a, wpr);
 }
@@ -616,8 +692,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM, true>())
     }
 }
 
-// The same for rows that start anywhere: wpr warps per token, a pair at a time, its row put
-// together as the row that is written lies (the token's forward, the pair's own backward).
+// The same for rows that start anywhere: wpr warps per token, 128 elements per warp and turn, a
+// lane's 4 lying 32 apart as in the dispatch, those of 4 choices fetched before the first is used.
+// (Aligned pieces of 16 bytes, shifted into place, 1001 wide: bf16 65.8 us against 53.4, backward 100.7
+// against 74.8; fp32 77.4 against 71.4, 142 against 109.  100 wide: 187 against 90, 358 against 134.)
 template <typename T>
 __global__ void __launch_bounds__(32 * kRowWarps, 5)
     expert_combine_shifted_kernel(const __grid_constant__ CombineArgs a, int wpr)
@@ -629,28 +707,47 @@ __global__ void __launch_bounds__(32 * kRowWarps, 5)
     if (t >= a.tokens) return;
     int place = lane < a.choices ? a.slots[t * a.choices + lane] : -1;
     if (place >= a.max_rows) place = -1;
-    const float weight = a.weights && lane < a.choices ? a.weights[t * a.choices + lane] : 1.f;
-    const int width = a.width;
-    const T *y = reinterpret_cast<const T *>(a.y), *y_end = y + a.max_rows * width;
-    const T *resid = reinterpret_cast<const T *>(a.resid), *r_end = resid + a.tokens * width;
-    for (int c0 = warp % wpr * 256 - lead_of<false>(t, width); c0 < width; c0 += 256 * wpr) {
-        float acc[8] = {};
-        if (resid) load8<false>(resid + t * width, c0, width, resid, r_end, acc);
-        for (int j = 0; j < a.choices; ++j) {
-            const int s = __shfl_sync(kFullMask, place, j);
-            const float w = __shfl_sync(kFullMask, weight, j);
-            if (s < 0) continue;                           // (warp-uniform)
-            float v[8];
-            load8<false>(y + (int64_t)s * width, c0, width, y, y_end, v);
+    const float weight = a.weights && place >= 0 ? a.weights[t * a.choices + lane] : 1.f;
+    const T *y = reinterpret_cast<const T *>(a.y);
+    const T *resid = a.resid ? reinterpret_cast<const T *>(a.resid) + t * a.width : nullptr;
+    T *out = reinterpret_cast<T *>(a.out) + t * a.width;
+    int s[4];
+    float w[4];
+    auto places = [&](int j0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        for (int u = 0; u < 4; ++u) {
+            s[u] = __shfl_sync(kFullMask, place, j0 + u);
+            w[u] = s[u] < 0 ? 0.f : __shfl_sync(kFullMask, weight, j0 + u);    // (warp-uniform)
         }
-        store8<false>(reinterpret_cast<T *>(a.out) + t * width, c0, width, acc);
+    };
+    places(0);
+    for (int c0 = warp % wpr * 128; c0 < a.width; c0 += 128 * wpr) {
+        const int c = c0 + lane, n = (a.width - c + 31) >> 5;  // elements from c on, 32 apart
+        typename ElemBits<T>::type r[kLaneElems], v[4][kLaneElems];
+        load_apart(resid + c, resid ? n : 0, r);
+        float acc[kLaneElems];
+        for (int j0 = 0;;) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) load_apart(y + (int64_t)s[u] * a.width + c, s[u] >= 0 ? n : 0, v[u]);
+#pragma unroll
+            for (int i = 0; i < kLaneElems; ++i) {
+                if (j0 == 0) acc[i] = elem(r[i]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[i] = fmaf(w[u], elem(v[u][i]), acc[i]);
+            }
+            j0 += 4;
+            if (j0 < a.choices) places(j0);
+            else break;
+        }
+        if (a.choices > 4) places(0);
+#pragma unroll
+        for (int i = 0; i < kLaneElems; ++i)
+            if (i < n) store_elem(out + c + 32 * i, acc[i]);
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kRowWarps, 5)
+__global__ void __launch_bounds__(32 * kRowWarps, 4)
     expert_combine_bwd_shifted_kernel(const __grid_constant__ CombineArgs a, int wpr)
 {
     __shared__ float dots[kRowWarps][kMaxChoices];
@@ -661,32 +758,45 @@ __global__ void __launch_bounds__(32 * kRowWarps, 5)
     const bool live = t < a.tokens;
     int place = live && lane < a.choices ? a.slots[t * a.choices + lane] : -1;
     if (place >= a.max_rows) place = -1;
-    const float weight = a.weights && live && lane < a.choices ? a.weights[t * a.choices + lane] : 1.f;
-    const int width = a.width;
-    const T *y = reinterpret_cast<const T *>(a.y), *y_end = y + a.max_rows * width;
-    const T *dout = reinterpret_cast<const T *>(a.dout), *g_end = dout + a.tokens * width;
+    const float weight = a.weights && place >= 0 ? a.weights[t * a.choices + lane] : 1.f;
+    const T *y = reinterpret_cast<const T *>(a.y);
+    const T *dout = reinterpret_cast<const T *>(a.dout) + (live ? t * a.width : 0);
     T *dy = reinterpret_cast<T *>(a.dy);
     float mine = 0.f;                                      // lane j: the dot product of pair j
-    for (int j = 0; j < a.choices; ++j) {
-        const int s = __shfl_sync(kFullMask, place, j);
-        const float w = __shfl_sync(kFullMask, weight, j);
-        if (s < 0) continue;                               // (warp-uniform)
-        float d = 0.f;
-        for (int c0 = warp % wpr * 256 - lead_of<false>(s, width); c0 < width; c0 += 256 * wpr) {
-            float g[8], o[8];
-            load8<false>(dout + t * width, c0, width, dout, g_end, g);
-            if (a.dweights) {
-                float v[8];
-                load8<false>(y + (int64_t)s * width, c0, width, y, y_end, v);
+    for (int j0 = 0; live && j0 < a.choices; j0 += 4) {
+        int s[4];
+        float w[4], d[4] = {};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d = fmaf(g[e], v[e], d);
+        for (int u = 0; u < 4; ++u) {
+            s[u] = __shfl_sync(kFullMask, place, j0 + u);
+            w[u] = __shfl_sync(kFullMask, weight, j0 + u);
+        }
+        for (int c = warp % wpr * 128 + lane; c < a.width; c += 128 * wpr) {
+            const int n = (a.width - c + 31) >> 5;
+            typename ElemBits<T>::type g[kLaneElems], v[4][kLaneElems];
+            load_apart(dout + c, n, g);
+            if (a.dweights) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) load_apart(y + (int64_t)s[u] * a.width + c, s[u] >= 0 ? n : 0, v[u]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = w * g[e];
-            store8<false>(dy + (int64_t)s * width, c0, width, o);
+            for (int u = 0; u < 4; ++u) {
+                if (s[u] < 0) continue;                    // (warp-uniform)
+                T *to = dy + (int64_t)s[u] * a.width + c;
+#pragma unroll
+                for (int i = 0; i < kLaneElems; ++i) {
+                    const float x = elem(g[i]);
+                    if (a.dweights) d[u] = fmaf(x, elem(v[u][i]), d[u]);
+                    if (i < n) store_elem(to + 32 * i, w[u] * x);
+                }
+            }
         }
-        d = warp_sum(d);
-        if (lane == j) mine = d;
+        if (!a.dweights) continue;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float sum = warp_sum(d[u]);
+            if (lane == j0 + u) mine = sum;
+        }
     }
     if (!a.dweights) return;
     if (lane < a.choices) dots[warp][lane] = mine;
