@@ -262,6 +262,13 @@ int warps_per_row(int64_t pieces, int per_lane)
 constexpr int kLaneElems = 4;
 
 // An element as it lies in memory, if `yes`, else 0.  (Inline for the reason at load16_if.)
+__device__ __forceinline__ void load_elem(const void *p, bool yes, uint8_t &v)
+{
+    uint16_t w;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t@q ld.global.b8 %0, [%1];\n\t}"
+                 : "=&h"(w) : "l"(p), "r"((int)yes));
+    v = (uint8_t)w;
+}
 __device__ __forceinline__ void load_elem(const void *p, bool yes, uint16_t &v)
 {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t@q ld.global.b16 %0, [%1];\n\t}"
@@ -334,62 +341,10 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     }
 }
 
-// Rows of an odd number of bytes, 512 bytes per warp and turn.  A lane keeps an aligned piece of the
-// token's row and its two neighbours; where each place lies decides which two of them hold an
-// aligned piece there, and by how much they shift.
-__global__ void __launch_bounds__(32 * kRowWarps)
-    expert_dispatch_shifted_kernel(const __grid_constant__ DispatchArgs a, int wpr)
-{
-    grid_dep_wait();
-    grid_dep_release();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * (kRowWarps / wpr) + warp / wpr;
-    if (t >= a.tokens) return;
-    const int part = warp % wpr;
-    int mine = lane < a.choices ? a.slots[t * a.choices + lane] : -1;
-    if (mine >= a.max_rows) mine = -1;
-    const uint8_t *src = a.x + t * a.row_bytes, *end = a.x + a.tokens * a.row_bytes;
-    const int from = (int)(reinterpret_cast<uintptr_t>(src) & 15);
-    // (places lie up to 15 bytes in front of their pieces' row, so the last piece may be one further)
-    for (int64_t c0 = part * 512; c0 < a.row_bytes + 15; c0 += 512 * wpr) {
-        const uint8_t *at = src - from + c0;
-        uint32_t x[12] = {}, edge[4] = {};               // the pieces before, at and behind `at`
-        load_piece(at + 16 * lane, a.x, end, x + 4);
-        if (lane == 0 || lane == 31) load_piece(lane ? at + 512 : at - 16, a.x, end, edge);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = __shfl_up_sync(kFullMask, x[4 + i], 1);
-            const uint32_t d = __shfl_down_sync(kFullMask, x[4 + i], 1);
-            x[i] = lane ? u : edge[i];
-            x[8 + i] = lane < 31 ? d : edge[i];
-        }
-        for (int j = 0; j < a.choices; ++j) {
-            const int s = __shfl_sync(kFullMask, mine, j);
-            if (s < 0) continue;
-            uint8_t *dst = a.out + (int64_t)s * a.row_bytes, *to = dst + a.row_bytes;
-            const int lead = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = from < lead ? x[i] : x[4 + i];
-            shift_words<8, 2>(v, (from - lead) & 15);
-            uint8_t *p = dst - lead + c0 + 16 * lane;
-            if (p >= dst && p + 16 <= to) *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
-            else if (p + 16 > dst && p < to) store_cut<4, 1>(p, v, dst, to);
-        }
-    }
-    if (part != 0 || !a.scales) return;
-    for (int j = 0; j < a.choices; ++j) {
-        const int s = __shfl_sync(kFullMask, mine, j);
-        if (s < 0) continue;
-        for (int g = lane; g < a.n_scales; g += 32)
-            a.scales_out[(int64_t)s * a.n_scales + g] = a.scales[t * a.n_scales + g];
-    }
-}
-
-// Rows that start anywhere, of whole elements E (2, 4 or 8 bytes): 128 elements per warp and turn, a
+// Rows that start anywhere, of whole elements E (1 to 8 bytes): 128 elements per warp and turn, a
 // lane's 4 lying 32 apart.  One element per access is what all alignments have in common, and a
-// warp's access is still a run of neighbours.  (By shifted pieces, as bytes go, 16384 x 4 places:
-// 1001 bf16 46.4 us against 36.9, 1003 fp32 82 against 57.)
+// warp's access is still a run of neighbours.  (By aligned pieces of 16 bytes, shifted into place,
+// 16384 x 4 places: 1001 bf16 46.4 us against 36.9, 1003 fp32 82 against 57, 1001 bytes 42 against 34.)
 template <typename E>
 __global__ void __launch_bounds__(32 * kRowWarps)
     expert_dispatch_apart_kernel(const __grid_constant__ DispatchArgs a, int wpr)
@@ -482,7 +437,7 @@ cudaError_t run_dispatch(const DispatchArgs &a, cudaStream_t st)
              : sizeof(V) == 8 ? expert_dispatch_apart_kernel<uint64_t>
              : sizeof(V) == 4 ? expert_dispatch_apart_kernel<uint32_t>
              : sizeof(V) == 2 ? expert_dispatch_apart_kernel<uint16_t>
-                              : expert_dispatch_shifted_kernel;
+                              : expert_dispatch_apart_kernel<uint8_t>;
     return launch_pdl(k, dim3((unsigned)((a.tokens + tokens - 1) / tokens)), dim3(32 * kRowWarps), 0,
                       st, a, wpr);
 }
