@@ -381,8 +381,8 @@ hstu_status_t hstu_rms_norm_rows_bwd(const void *dy, const void *sum, const floa
  *
  * hstu_expert_combine: out_t = residual_t + sum over j of weights[t, j] * y[slots[t, j]], summed
  * in fp32 in the order of j; y [max_rows, width], out and residual (NULL: none) [tokens, width] of
- * `dtype`, weights [tokens, choices] fp32 (NULL: ones).  Without weights and residual it is the
- * gradient of hstu_expert_dispatch.
+ * `dtype`, weights [tokens, choices] fp32 (NULL: ones); width in 1..2^30; out may be residual itself.
+ * Without weights and residual it is the gradient of hstu_expert_dispatch.
  *
  * hstu_expert_combine_bwd: dy[slots[t, j]] = weights[t, j] * dout_t (rows of dy that no slot names
  * are left as they were) and dweights[t, j] = <dout_t, y[slots[t, j]]> (0 for pairs without a

@@ -681,7 +681,8 @@ hstu_status_t hstu_expert_combine(const void *y, const int32_t *slots, const flo
                                   int64_t max_rows, int32_t width, int32_t dtype, void *out,
                                   void *stream)
 {
-    if (!route_shape_ok(tokens, choices) || max_rows < 0 || width < 1 || !dtype_ok(dtype))
+    if (!route_shape_ok(tokens, choices) || max_rows < 0 || width < 1 || width > kMaxCombineWidth ||
+        !dtype_ok(dtype))
         return HSTU_ERR_INVALID_ARGUMENT;
     if (tokens == 0) return HSTU_OK;
     if ((max_rows > 0 && !y) || !slots || !out ||
@@ -698,7 +699,8 @@ hstu_status_t hstu_expert_combine_bwd(const void *dout, const void *y, const int
                                       int64_t max_rows, int32_t width, int32_t dtype, void *dy,
                                       float *dweights, void *stream)
 {
-    if (!route_shape_ok(tokens, choices) || max_rows < 0 || width < 1 || !dtype_ok(dtype))
+    if (!route_shape_ok(tokens, choices) || max_rows < 0 || width < 1 || width > kMaxCombineWidth ||
+        !dtype_ok(dtype))
         return HSTU_ERR_INVALID_ARGUMENT;
     if (tokens == 0) return HSTU_OK;
     if (!dout || !slots || (max_rows > 0 && (!dy || (dweights && !y))) ||

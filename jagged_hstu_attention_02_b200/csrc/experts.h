@@ -71,6 +71,7 @@ cudaError_t launch_rms_norm_bwd(const RmsBwdArgs &a, bool f32, cudaStream_t st);
 // ------------------------------------------------------------------ experts.cu
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 16;
+constexpr int kMaxCombineWidth = 1 << 30;   // (element counters of a row step past its end in 32 bits)
 
 struct SortArgs {
     const void *ids;            // [n] int32 or int64

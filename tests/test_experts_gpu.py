@@ -392,6 +392,34 @@ def test_combine_skips_places_outside_and_dispatch_bwd_sums():
         assert not ops.expert_combine(none, slots, torch.full((3, 2), float("nan"), device="cuda")).any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,k,width", [(700, 4, 1001), (5000, 3, 100), (90, 9, 2047), (3000, 2, 1024)])
+def test_combine_over_its_residual_and_of_many_rows(T, k, width, dtype):
+    """More tokens than blocks at once; the result written over the residual; rows that no slot
+    names hold NaN."""
+    rng = np.random.default_rng(T)
+    r = ops.expert_sort(torch.from_numpy(_ids(rng, T, k, 16)).cuda(), 16)
+    n = int(r.offsets[-1])
+    y, res = _rand(1, T * k, width, dtype=dtype), _rand(2, T, width, dtype=dtype)
+    y[n:] = float("nan")
+    w = torch.rand(T, k, device="cuda")
+    slots = r.slots.long()
+    live = (slots >= 0).double()[..., None]
+    rows = torch.nan_to_num(y.double()[slots.clamp_min(0)]) * live
+    want = res.double() + (w.double()[..., None] * rows).sum(1)
+    size = res.double().abs() + (w.double()[..., None] * rows.abs()).sum(1)
+    out = res.clone()
+    ops.expert_combine(y, r.slots, w, residual=out, out=out)
+    _close(out, _np(want), _np(want.abs() * HALF[dtype] + size * (k + 1) * U), "over the residual")
+    dout = _rand(3, T, width, dtype=dtype)
+    dy, dw = ops.expert_combine_bwd(dout, y, r.slots, w)
+    dots = (dout.double()[:, None, :] * rows).sum(2)
+    mag = (dout.double()[:, None, :] * rows).abs().sum(2)
+    _close(dw, _np(dots), _np(mag) * (width / 32 + 12) * U, "dweights")
+    sorted_dy = (w.double()[..., None] * dout.double()[:, None, :])[slots >= 0]
+    _close(dy[slots[slots >= 0]], _np(sorted_dy), _np(sorted_dy.abs()) * HALF[dtype] + 1e-40, "dy")
+
+
 # ------------------------------------------------------------------ products
 
 def _offsets(counts):

@@ -145,6 +145,13 @@ def test_routing_refusals():
         assert cbwd(**bad) == INVALID, bad
 
 
+def test_combine_refuses_rows_whose_counters_would_overflow():
+    L = ops.lib()
+    for width in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert L.hstu_expert_combine(_p(), _p(), None, None, 4, 2, 8, width, 1, _p(), None) == INVALID
+        assert L.hstu_expert_combine_bwd(_p(), _p(), _p(), None, 4, 2, 8, width, 1, _p(), None, None) == INVALID
+
+
 def test_product_refusals():
     L = ops.lib()
 
