@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM, true>())
 // against 74.8; fp32 77.4 against 71.4, 142 against 109.  100 wide: 187 against 90, 358 against 134.)
 template <typename T>
 __global__ void __launch_bounds__(32 * kRowWarps, 5)
-    expert_combine_shifted_kernel(const __grid_constant__ CombineArgs a, int wpr)
+    expert_combine_apart_kernel(const __grid_constant__ CombineArgs a, int wpr)
 {
     grid_dep_wait();
     grid_dep_release();
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 5)
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kRowWarps, 4)
-    expert_combine_bwd_shifted_kernel(const __grid_constant__ CombineArgs a, int wpr)
+    expert_combine_bwd_apart_kernel(const __grid_constant__ CombineArgs a, int wpr)
 {
     __shared__ float dots[kRowWarps][kMaxChoices];
     grid_dep_wait();
@@ -781,7 +781,7 @@ cudaError_t run_combine(const CombineArgs &a, cudaStream_t st)
     if (a.width % 8 != 0) {
         const int wpr = warps_per_row((a.width + 7) / 8, 4);
         const int64_t per = kRowWarps / wpr;
-        return launch_pdl(BWD ? expert_combine_bwd_shifted_kernel<T> : expert_combine_shifted_kernel<T>,
+        return launch_pdl(BWD ? expert_combine_bwd_apart_kernel<T> : expert_combine_apart_kernel<T>,
                           dim3((unsigned)((a.tokens + per - 1) / per)), dim3(32 * kRowWarps), 0, st, a,
                           wpr);
     }
