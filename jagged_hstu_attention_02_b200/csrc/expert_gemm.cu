@@ -442,20 +442,32 @@ __device__ __forceinline__ ETile tile_of(const EGemmArgs &a, const ExpertTable &
     return r;
 }
 
+// a b, results below the normal numbers 0.
+__device__ __forceinline__ float mul_ftz(float a, float b)
+{
+    float r;
+    asm("mul.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // sigmoid(x) and sigmoid(y) on the hardware's exponential and reciprocal (2 ulp each), one
 // reciprocal for both: 1 / a = b / (a b).  The special-function unit takes 8 cycles per warp and
 // call, so 4 calls for two values of a 256-wide tile would outlast its MMAs below 512 of the
-// contraction.  Exponents stop at 2^62 (x = -43), where the product would leave fp32's range:
-// from there on sigmoid is 2^-62 instead of less, an error of x SiLU(x) below 1e-17.
+// contraction.  a and b = 1 + exp(-.) are kept times 2^-63, so that a b stays in fp32's range up to
+// where exponents stop, at 2^126.5 (x = -87.7).  There 1 / a is 2^-126.5, which the last product
+// flushes to 0: x sigmoid(x) is 0 for any x from there down, and the other value does not notice.
+// With both far down (a b above 2^189) both are 0, an error of x sigmoid(x) below 1e-17.
 __device__ __forceinline__ void sigmoid2(float x, float y, float &sx, float &sy)
 {
+    constexpr float kDown = 0x1p-63f;
     float ex, ey, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(fminf(x * -1.4426950408889634f, 62.f)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(fminf(y * -1.4426950408889634f, 62.f)));
-    const float a = 1.f + ex, b = 1.f + ey;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(fminf(x * -1.4426950408889634f, 126.5f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(fminf(y * -1.4426950408889634f, 126.5f)));
+    const float a = fmaf(ex, kDown, kDown), b = fmaf(ey, kDown, kDown);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-    sx = r * b;
-    sy = r * a;
+    r = mul_ftz(r, kDown);
+    sx = mul_ftz(r, b);
+    sy = mul_ftz(r, a);
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&f)[8])

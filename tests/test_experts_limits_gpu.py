@@ -1,0 +1,119 @@
+"""The mixture-of-experts operators at the ends of their ranges, against formulas in 64 bits.
+
+Tolerances count roundings as in test_experts_gpu.py: half a step of the output type relative to
+the value (bf16 2^-8, e4m3 2^-4), 2^-14 for the fast exponential of SiLU and its slope.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from jagged_hstu_attention_02_b200 import ops
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+# ------------------------------------------------------------------ SiLU far from zero
+
+# rows of each expert, and the contraction, of the products' three kernels: single blocks (128 x 128
+# tiles), pairs of blocks, blocks that share a tile's contraction.  16384 rows of two experts make
+# pairs; 17 slices of the contraction and 12 tiles make 8 blocks share each.
+KERNELS = {"single": ([100, 97], 1), "pair": ([11000, 9001], 1), "shared": ([64, 65], 17)}
+WIDE = 512
+
+
+def _far(lo, hi, n=WIDE):
+    """[n] bf16 values: far ones of lo .. hi beside ordinary ones in neighbouring columns, on
+    either side, and beside one another."""
+    far = [lo, hi] + [float(v) for v in np.geomspace(abs(lo), abs(hi), 11)[1:-1] * np.sign(lo)]
+    g = torch.Generator().manual_seed(11)
+    v = torch.randn(n, generator=g) * 4
+    f = torch.tensor(far)
+    i = torch.arange(n)
+    v = torch.where(i % 4 == 0, f[i // 4 % len(far)], v)              # far, ordinary
+    v = torch.where(i % 8 == 7, f[(i // 8 + 5) % len(far)], v)        # ordinary, far
+    v = torch.where(i % 16 == 1, f[(i // 16 + 3) % len(far)], v)      # far, far
+    return v.to(BF)
+
+
+def _silu64(v):
+    v = v.double()
+    return torch.where(v < -700, 0.0 * v, v / (1 + torch.exp(-v)))
+
+
+def _slope64(v):
+    """sigma(v) (1 + v (1 - sigma(v))); 1 and 0 far from zero, where the terms leave their range."""
+    v = v.double()
+    c = v.clamp(-700, 700)
+    p = 1 / (1 + torch.exp(-c))
+    return p * (1 + c / (1 + torch.exp(c)))
+
+
+def _offsets(counts):
+    return torch.tensor([0] + counts, device="cuda").cumsum(0)
+
+
+def _far_product(kernel, v, e4m3):
+    """Rows whose product with either expert's matrix is v in every row: (x, w, offsets), in 8 bits
+    (x, its scales, w, its scales, offsets).  One term of the contraction is not zero, so the
+    product is exact."""
+    counts, slices = KERNELS[kernel]
+    K = (16 if e4m3 else 8) if slices == 1 else slices * (128 if e4m3 else 64)
+    S, E = sum(counts), len(counts)
+    at = K - 3
+    if e4m3:
+        x = torch.zeros(S, K, device="cuda")
+        w = torch.zeros(E, WIDE, K, device="cuda")
+        x[:, at], w[:, :, at] = 2.0, 0.5
+        ws = v.float().cuda().expand(E, WIDE).contiguous()
+        return x.to(ops.F8), torch.ones(S, device="cuda"), w.to(ops.F8), ws, _offsets(counts)
+    x, w = torch.zeros(S, K, device="cuda", dtype=BF), torch.zeros(E, K, WIDE, device="cuda", dtype=BF)
+    x[:, at], w[:, at, :] = 1.0, v.cuda()
+    return x, w, _offsets(counts)
+
+
+def _rows_match(got, want, tol, what):
+    got = got.double()
+    bad = ~((got - want.cuda()).abs() <= tol.cuda())               # (NaN is bad)
+    at = torch.nonzero(bad)
+    assert not len(at), "%s: %g for %g at %s" % (
+        what, got[tuple(at[0])], want[at[0][1]], tuple(at[0].tolist()))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("lo,hi", [(-30.0, -60.0), (-100.0, -1e6), (-1e12, -3e38)])
+def test_silu_and_its_slope_of_large_negative_values_go_to_zero(kernel, lo, hi):
+    """Far down the result is 0, off by at most 43 2^-62 < 1e-17 where that begins."""
+    v = _far(lo, hi)
+    want = _silu64(v)
+    tol = want.abs() * (2 ** -8 + 2 ** -14) + 1e-17
+    x, w, off = _far_product(kernel, v, False)
+    pre = torch.empty(x.shape[0], WIDE, dtype=BF, device="cuda")
+    out = ops.expert_proj(x, w, off, silu=True, pre=pre)
+    assert torch.equal(pre, v.cuda().expand_as(pre))
+    _rows_match(out, want, tol, "silu")
+    x, xs, w, ws, off = _far_product(kernel, v, True)
+    _rows_match(ops.expert_proj_e4m3(x, xs, w, ws, off, silu=True), want, tol, "silu, 8 bits")
+    _check_slope(kernel, v)
+
+
+def _check_slope(kernel, v):
+    counts, slices = KERNELS[kernel]
+    N, S, E = 8 if slices == 1 else slices * 64, sum(counts), len(counts)
+    dout, w = torch.zeros(S, N, device="cuda", dtype=BF), torch.zeros(E, WIDE, N, device="cuda", dtype=BF)
+    dout[:, N - 3], w[:, :, N - 3] = 1.0, 1.5
+    silu_pre = v.cuda().expand(S, WIDE).contiguous()
+    dx, _ = ops.expert_proj_bwd(dout, torch.zeros_like(silu_pre), w, _offsets(counts), silu_pre=silu_pre,
+                                grads=(torch.empty_like(silu_pre), None))
+    # the slope is a sum of terms of at most 1.1, each within 2^-14 of its value
+    want = 1.5 * _slope64(v)
+    _rows_match(dx, want, want.abs() * 2 ** -8 + 1.5 * 2 ** -14 * (v.double().abs() < 43) *
+                _slope_terms(v) + 1e-17, "slope")
+
+
+def _slope_terms(v):
+    c = v.double().clamp(-700, 700)
+    p = 1 / (1 + torch.exp(-c))
+    return p * (1 + c.abs() / (1 + torch.exp(c)))
