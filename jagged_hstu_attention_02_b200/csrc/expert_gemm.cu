@@ -457,7 +457,10 @@ __device__ __forceinline__ float mul_ftz(float a, float b)
 // where exponents stop, at 2^126.5 (x = -87.7).  There 1 / a is 2^-126.5, which the last product
 // flushes to 0: x sigmoid(x) is 0 for any x from there down, and the other value does not notice.
 // With both far down (a b above 2^189) both are 0, an error of x sigmoid(x) below 1e-17.
-__device__ __forceinline__ void sigmoid2(float x, float y, float &sx, float &sy)
+// rx, ry: 1 - sigmoid, as exp(-x) sigmoid(x), which goes to 0 with exp(-x) (and is 0 where sigmoid
+// is: its users multiply by that).  1.f - sx would keep the reciprocal's rounding, which depends on
+// the other value, and times x = 1e6 or more that rounding is what the slope of SiLU would be.
+__device__ __forceinline__ void sigmoid2(float x, float y, float &sx, float &sy, float &rx, float &ry)
 {
     constexpr float kDown = 0x1p-63f;
     float ex, ey, r;
@@ -468,6 +471,8 @@ __device__ __forceinline__ void sigmoid2(float x, float y, float &sx, float &sy)
     r = mul_ftz(r, kDown);
     sx = mul_ftz(r, b);
     sy = mul_ftz(r, a);
+    rx = ex * sx;
+    ry = ey * sy;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&f)[8])
@@ -520,10 +525,10 @@ __device__ __forceinline__ uint4 convert8(const EGemmArgs &a, float xs, const fl
             for (int y = 0; y < 4; ++y) {
                 const float p0 = __uint_as_float(u4[y] << 16);
                 const float p1 = __uint_as_float(u4[y] & 0xFFFF0000u);
-                float g0, g1;
-                sigmoid2(p0, p1, g0, g1);
-                f[2 * y] *= g0 * fmaf(p0, 1.f - g0, 1.f);
-                f[2 * y + 1] *= g1 * fmaf(p1, 1.f - g1, 1.f);
+                float g0, g1, r0, r1;
+                sigmoid2(p0, p1, g0, g1, r0, r1);
+                f[2 * y] *= g0 * fmaf(p0, r0, 1.f);
+                f[2 * y + 1] *= g1 * fmaf(p1, r1, 1.f);
             }
         }
     }
@@ -531,8 +536,8 @@ __device__ __forceinline__ uint4 convert8(const EGemmArgs &a, float xs, const fl
         if (a.silu && !product) {
 #pragma unroll
             for (int x = 0; x < 8; x += 2) {
-                float g0, g1;
-                sigmoid2(f[x], f[x + 1], g0, g1);
+                float g0, g1, r0, r1;
+                sigmoid2(f[x], f[x + 1], g0, g1, r0, r1);
                 f[x] *= g0;
                 f[x + 1] *= g1;
             }

@@ -117,3 +117,14 @@ def _slope_terms(v):
     c = v.double().clamp(-700, 700)
     p = 1 / (1 + torch.exp(-c))
     return p * (1 + c.abs() / (1 + torch.exp(c)))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("lo,hi", [(20.0, 300.0), (1e3, 1e6), (1e7, 3e38)])
+def test_silu_of_large_positive_values_is_the_value_and_its_slope_one(kernel, lo, hi):
+    """Whatever stands in the column beside them."""
+    v = _far(lo, hi)
+    want = _silu64(v)
+    x, w, off = _far_product(kernel, v, False)
+    _rows_match(ops.expert_proj(x, w, off, silu=True), want, want.abs() * (2 ** -8 + 2 ** -14), "silu")
+    _check_slope(kernel, v)
