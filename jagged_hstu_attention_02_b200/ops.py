@@ -501,7 +501,8 @@ def rms_norm_rows(x, weight=None, residual=None, *, eps=1e-5, e4m3=False, group=
                   training=False, out: Optional[RmsNorm] = None, stream=None) -> RmsNorm:
     """RMS norm of the rows of h = x (+ residual), times weight (fp32).  e4m3: y in 8 bits with
     one fp32 scale per row (group 0) or per `group` (32, 64, 128) columns, y ~ q * scale.
-    training keeps rstd for rms_norm_rows_bwd.  out: a result to write into again."""
+    training keeps rstd for rms_norm_rows_bwd.  out: a result to write into again; its sum only
+    with a residual (the sum of a call without one is that call's x)."""
     dev = x.get_device()
     if _elsewhere(dev, stream):
         with _place(dev, stream):
@@ -533,6 +534,8 @@ def rms_norm_rows(x, weight=None, residual=None, *, eps=1e-5, e4m3=False, group=
         pst = _expect(out.rstd, "out.rstd", torch.float32, (rows,), dev)
         if (e4m3 and psc is None) or (training and pst is None):
             raise ValueError("out lacks scales or rstd")
+        out = RmsNorm(out.y, out.scales if e4m3 else None, x if residual is None else out.sum,
+                      out.rstd)
     if residual is None:
         psum = None
     if e4m3:

@@ -128,3 +128,26 @@ def test_silu_of_large_positive_values_is_the_value_and_its_slope_one(kernel, lo
     x, w, off = _far_product(kernel, v, False)
     _rows_match(ops.expert_proj(x, w, off, silu=True), want, want.abs() * (2 ** -8 + 2 ** -14), "silu")
     _check_slope(kernel, v)
+
+
+# ------------------------------------------------------------------ norm
+
+def test_norm_without_residual_into_an_earlier_result_keeps_the_rows_themselves():
+    """The sum of a norm without a residual is x: not what an earlier call left in `out`."""
+    g = torch.Generator().manual_seed(3)
+    x1, x2, res = ((torch.randn(40, 256, generator=g)).to(BF).cuda() for _ in range(3))
+    w = (1 + 0.2 * torch.randn(256, generator=g)).cuda()
+    dy = torch.randn(40, 256, generator=g).to(BF).cuda()
+    for first in (ops.rms_norm_rows(x1, w, training=True), ops.rms_norm_rows(x1, w, res, training=True)):
+        kept = x1.clone(), first.sum.clone()
+        r = ops.rms_norm_rows(x2, w, training=True, out=first)
+        fresh = ops.rms_norm_rows(x2, w, training=True)
+        assert r.y is first.y and r.rstd is first.rstd             # written again
+        assert torch.equal(r.y, fresh.y) and torch.equal(r.rstd, fresh.rstd)
+        assert torch.equal(r.sum, x2)
+        for a, b in zip(ops.rms_norm_rows_bwd(dy, r.sum, r.rstd, w),
+                        ops.rms_norm_rows_bwd(dy, fresh.sum, fresh.rstd, w)):
+            assert torch.equal(a, b)
+        assert torch.equal(x1, kept[0]) and torch.equal(first.sum, kept[1])
+    r = ops.rms_norm_rows(x2, w, res, training=True, out=ops.rms_norm_rows(x1, w, res, training=True))
+    assert torch.equal(r.sum, ops.rms_norm_rows(x2, w, res).sum)
