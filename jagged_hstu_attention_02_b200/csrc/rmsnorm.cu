@@ -64,12 +64,13 @@ __device__ __forceinline__ float scale_top(float m)
     return m > 0.f ? fmaxf(m, 7.888609e-31f /* 2^-100 */) : 0.f;
 }
 
-// 448 / m to 2 ulp (m is 0 or in the range of normal numbers).  Of 451 M values 302 come out one e4m3
-// step from those of exact arithmetic, 362 with every operation rounded to nearest; a step of Newton's
-// here makes that 261 and 16384 x 4096 bf16 3 % slower.
+// 448 / m to 2 ulp, for m = 0 or from 2^-100 on.  (The fast division gives 0 for divisors above 2^126:
+// both are taken by 4.)  Of 451 M values 302 come out one e4m3 step from those of exact arithmetic,
+// 362 with every operation rounded to nearest; a step of Newton's here makes that 261 and
+// 16384 x 4096 bf16 3 % slower.
 __device__ __forceinline__ float scale_back(float m)
 {
-    return m > 0.f ? __fdividef(kE4m3Max, m) : 0.f;
+    return m > 0.f ? __fdividef(kE4m3Max * 0.25f, m * 0.25f) : 0.f;
 }
 
 // rs as a power of two times a factor in [1, 2).  The 8-bit values do not depend on the factor: it

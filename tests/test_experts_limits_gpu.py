@@ -151,3 +151,24 @@ def test_norm_without_residual_into_an_earlier_result_keeps_the_rows_themselves(
         assert torch.equal(x1, kept[0]) and torch.equal(first.sum, kept[1])
     r = ops.rms_norm_rows(x2, w, res, training=True, out=ops.rms_norm_rows(x1, w, res, training=True))
     assert torch.equal(r.sum, ops.rms_norm_rows(x2, w, res).sum)
+
+
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("rows,width", [(3, 512), (3, 509), (6000, 512), (6000, 509)])
+def test_norm_e4m3_of_the_largest_and_smallest_values(rows, width, group):
+    """y = weight here (rows of +-1, eps 0).  Groups with a maximum in (2^126, 2^128), where a
+    fast division of 448 by it would give 0, and groups below 2^-100, whose scale is that of
+    2^-100: 2^-100 / 448 within 2^-17."""
+    g = torch.Generator().manual_seed(width)
+    sign = (2 * torch.randint(0, 2, (rows, width), generator=g) - 1).float()
+    for top in (3.4e38, 1.8e38, 9e37, 8e37, 1e-20, 1e-33):
+        w = torch.rand(width, generator=g) * 0.9 * top
+        w[::16] = top
+        r = ops.rms_norm_rows(sign.cuda(), w.cuda(), eps=0.0, e4m3=True, group=group)
+        y = (sign * w).double()
+        want = torch.full((rows, r.scales.shape[1]), max(float(w.max()), 2.0 ** -100) / 448, dtype=torch.float64)
+        assert ((r.scales.double().cpu() - want).abs() <= want * 2 ** -17).all(), top
+        v = y / want[0, 0]
+        got = r.y.float().double().cpu()
+        tol = torch.maximum(v.abs() * 2 ** -4, torch.tensor(2.0 ** -10)) + v.abs() * 2 ** -17
+        assert ((got - v).abs() <= tol).all(), (top, got[0, :4], v[0, :4])
