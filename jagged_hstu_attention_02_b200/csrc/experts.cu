@@ -239,10 +239,9 @@ cudaError_t run_sort(const SortArgs &a, cudaStream_t st)
         return launch_pdl(expert_place_kernel<I, true>, dim3(1), dim3(kSortThreads), smem, st, a);
     }
     e = allow_smem<expert_count_kernel<I>>(smem);
-    if (e != cudaSuccess) return e;
+    if (e == cudaSuccess) e = allow_smem<expert_place_kernel<I, false>>(smem);
+    if (e != cudaSuccess) return e;                       // (before the first launch)
     e = launch_pdl(expert_count_kernel<I>, dim3(blocks), dim3(kSortThreads), smem, st, a);
-    if (e != cudaSuccess) return e;
-    e = allow_smem<expert_place_kernel<I, false>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(expert_place_kernel<I, false>, dim3(blocks), dim3(kSortThreads), smem, st, a);
 }

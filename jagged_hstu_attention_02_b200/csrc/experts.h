@@ -12,14 +12,25 @@
 
 namespace hstu {
 
-// Lets `kern` use `bytes` of dynamic shared memory.  The attribute is raised once per kernel and
-// device (asking the runtime at every call took a fifth of a small call's time on the host).
+// Lets Kern use `bytes` of dynamic shared memory.  Without the attribute a block may have 48 KB,
+// what the kernel declares itself included.  Its own part is asked for once per kernel, and the
+// attribute raised once per kernel and device (asking the runtime at every call took a fifth of a
+// small call's time on the host).
 template <auto Kern>
 cudaError_t allow_smem(size_t bytes)
 {
     constexpr int kMaxDev = 64;
+    static std::atomic<int64_t> own{-1};
     static std::atomic<size_t> allowed[kMaxDev];
-    if (bytes <= 48 * 1024) return cudaSuccess;          // every kernel may use that much
+    int64_t fixed = own.load(std::memory_order_relaxed);
+    if (fixed < 0) {
+        cudaFuncAttributes fa;
+        const cudaError_t e = cudaFuncGetAttributes(&fa, Kern);
+        if (e != cudaSuccess) return e;
+        fixed = (int64_t)fa.sharedSizeBytes;
+        own.store(fixed, std::memory_order_relaxed);
+    }
+    if (bytes + (size_t)fixed <= 48 * 1024) return cudaSuccess;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -27,10 +38,7 @@ cudaError_t allow_smem(size_t bytes)
     int most = 0;
     e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, Kern);
-    if (e != cudaSuccess) return e;
-    const size_t room = (size_t)most - fa.sharedSizeBytes;
+    const size_t room = (size_t)(most - fixed);
     if (bytes > room) return cudaErrorInvalidValue;
     e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
     if (e != cudaSuccess) return e;

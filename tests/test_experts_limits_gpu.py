@@ -3,6 +3,9 @@
 Tolerances count roundings as in test_experts_gpu.py: half a step of the output type relative to
 the value (bf16 2^-8, e4m3 2^-4), 2^-14 for the fast exponential of SiLU and its slope.
 """
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -13,6 +16,7 @@ from jagged_hstu_attention_02_b200 import ops
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 # ------------------------------------------------------------------ SiLU far from zero
@@ -172,3 +176,33 @@ def test_norm_e4m3_of_the_largest_and_smallest_values(rows, width, group):
         got = r.y.float().double().cpu()
         tol = torch.maximum(v.abs() * 2 ** -4, torch.tensor(2.0 ** -10)) + v.abs() * 2 ** -17
         assert ((got - v).abs() <= tol).all(), (top, got[0, :4], v[0, :4])
+
+
+# ------------------------------------------------------------------ sort
+
+_SORT = """
+import numpy as np, torch
+from jagged_hstu_attention_02_b200 import ops
+rng = np.random.default_rng(1)
+for n in (2000, 5000):
+    for dtype in (np.int32, np.int64):
+        for E in (639, 640, 700, 767, 768, 769, 1024):
+            ids = rng.integers(-1, E, (n // 2, 2)).astype(dtype)
+            r = ops.expert_sort(torch.from_numpy(ids).cuda(), E)
+            flat = ids.reshape(-1)
+            order = np.argsort(np.where(flat < 0, E, flat), kind="stable")
+            m = int((flat >= 0).sum())
+            slots = np.full(n, -1)
+            slots[order[:m]] = np.arange(m)
+            ends = np.concatenate([[0], np.cumsum(np.bincount(flat[flat >= 0], minlength=E))])
+            assert np.array_equal(r.slots.cpu().numpy().reshape(-1), slots), (n, dtype, E)
+            assert np.array_equal(r.offsets.cpu().numpy(), ends), (n, dtype, E)
+            assert np.array_equal(r.rows.cpu().numpy()[:m], order[:m] // 2), (n, dtype, E)
+print("sorted")
+"""
+
+
+def test_sort_of_any_number_of_experts_in_a_new_process():
+    """The numbers of experts ascend: no earlier call has asked for more shared memory."""
+    r = subprocess.run([sys.executable, "-c", _SORT], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "sorted" in r.stdout, r.stderr[-2000:]
