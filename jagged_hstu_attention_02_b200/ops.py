@@ -451,6 +451,12 @@ def _expect(t, name, dtype, shape, dev):
     return t.data_ptr()
 
 
+def _expect_32(*sizes):
+    """Sizes that the C ABI takes as 32 bits (ctypes would cut larger ones)."""
+    if max(sizes) >= 2 ** 31:
+        raise ValueError("a size of 2^31 or more: %s" % (sizes,))
+
+
 def _expect_rows(t, name):
     """(rows, width, dtype code) of a matrix of rows."""
     if t.dim() != 2:
@@ -459,6 +465,8 @@ def _expect_rows(t, name):
     if code is None:
         raise ValueError("unsupported dtype %s" % t.dtype)
     rows, width = t.shape
+    if width >= 2 ** 31:
+        _expect_32(width)
     return rows, width, code
 
 
@@ -601,6 +609,7 @@ def expert_sort(expert_ids, num_experts: int, *, status=None, out: Optional[Rout
     if dtype not in (torch.int32, torch.int64):
         raise ValueError("expert_ids must be int32 or int64")
     T, k = shape = expert_ids.shape
+    _expect_32(k, num_experts)
     pid = _expect(expert_ids, "expert_ids", dtype, shape, dev)
     pst = _expect_status(status, dev)
     _on_cuda(dev)
@@ -623,6 +632,8 @@ def _expect_slots(slots, dev):
     if slots.dim() != 2:
         raise ValueError("slots must be [tokens, choices]")
     T, k = shape = slots.shape
+    if k >= 2 ** 31:
+        _expect_32(k)
     return T, k, _expect(slots, "slots", torch.int32, shape, dev)
 
 
@@ -647,6 +658,7 @@ def expert_dispatch(x, slots, *, scales=None, out=None, scales_out=None, stream=
         if scales.dim() != 2:
             raise ValueError("scales must be [tokens, n]")
         n_scales = scales.shape[1]
+        _expect_32(n_scales)
         psc = _expect(scales, "scales", torch.float32, (T, n_scales), dev)
     _on_cuda(dev)
     if out is None:
@@ -719,6 +731,7 @@ def expert_dispatch_bwd(dxs, slots, *, out=None, stream=None):
 def _expect_proj(x, w):
     if x.dim() != 2 or w.dim() != 3:
         raise ValueError("x must be [rows, d_in] and w [experts, ., .]")
+    _expect_32(x.shape[1], *w.shape)
 
 
 def expert_proj(x, w, offsets, *, silu=False, pre=None, out=None, status=None, stream=None):

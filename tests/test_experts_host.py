@@ -235,3 +235,34 @@ def test_binding_refuses_wrong_shapes_types_and_places():
     for c in calls:
         with pytest.raises(ValueError):
             c()
+
+
+def test_binding_refuses_sizes_that_the_c_abi_would_cut_to_32_bits():
+    """2^32 + 64 columns are not 64: the tensors have no memory, and the size is refused first."""
+    wide, bf = 2 ** 32 + 64, torch.bfloat16
+
+    def empty(*shape, dtype=bf):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    one = empty(1, 1, dtype=torch.int32)
+    off, scale = empty(2, dtype=torch.int64), empty(1, dtype=torch.float32)
+    calls = [
+        lambda: ops.rms_norm_rows(empty(1, wide)),
+        lambda: ops.rms_norm_rows(empty(1, wide), e4m3=True, group=128),
+        lambda: ops.rms_norm_rows_bwd(empty(1, wide), empty(1, wide), scale),
+        lambda: ops.expert_sort(one, wide),
+        lambda: ops.expert_sort(empty(1, wide, dtype=torch.int32), 4),
+        lambda: ops.expert_dispatch(empty(1, 64), empty(1, wide, dtype=torch.int32)),
+        lambda: ops.expert_dispatch(empty(1, 64), one, scales=empty(1, wide, dtype=torch.float32)),
+        lambda: ops.expert_combine(empty(1, wide), one),
+        lambda: ops.expert_combine_bwd(empty(1, wide), empty(1, wide), one),
+        lambda: ops.expert_proj(empty(1, wide), empty(1, wide, 8), off),
+        lambda: ops.expert_proj(empty(1, 8), empty(1, 8, wide), off),
+        lambda: ops.expert_proj(empty(1, 8), empty(wide, 8, 8), empty(wide + 1, dtype=torch.int64)),
+        lambda: ops.expert_proj_e4m3(empty(1, wide, dtype=ops.F8), scale, empty(1, 8, wide, dtype=ops.F8),
+                                     empty(1, 8, dtype=torch.float32), off),
+        lambda: ops.expert_proj_bwd(empty(1, 8), empty(1, wide), empty(1, wide, 8), off),
+    ]
+    for c in calls:
+        with pytest.raises(ValueError, match="2.31 or more"):
+            c()
