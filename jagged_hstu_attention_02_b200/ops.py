@@ -672,8 +672,12 @@ def expert_dispatch(x, slots, *, scales=None, out=None, scales_out=None, stream=
             scales_out = scales.new_empty((most, n_scales))
         pso = _expect(scales_out, "scales_out", torch.float32, (most, n_scales), dev)
     row = shape[1:].numel()
+    if row == 0 and n_scales:                       # the scales are all there is to move
+        px, row, po, psc, pso = psc, 4 * n_scales, pso, None, None
+    else:
+        row *= x.element_size()
     if row:
-        _check(lib().hstu_expert_dispatch(px, row * x.element_size(), psc, n_scales, ps, T, k, most,
+        _check(lib().hstu_expert_dispatch(px, row, psc, n_scales, ps, T, k, most,
                                           po, pso, _raw_stream(dev)), "hstu_expert_dispatch")
     return out if scales is None else (out, scales_out)
 

@@ -206,3 +206,15 @@ def test_sort_of_any_number_of_experts_in_a_new_process():
     """The numbers of experts ascend: no earlier call has asked for more shared memory."""
     r = subprocess.run([sys.executable, "-c", _SORT], cwd=ROOT, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "sorted" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ dispatch
+
+def test_dispatch_of_rows_without_elements_moves_their_scales():
+    slots = torch.tensor([[2, 0], [-1, 1], [3, 9]], dtype=torch.int32, device="cuda")
+    x = torch.empty(3, 0, dtype=BF, device="cuda")
+    scales = torch.arange(12, device="cuda").float().view(3, 4)
+    out, got = ops.expert_dispatch(x, slots, scales=scales, scales_out=torch.full((6, 4), -1.0, device="cuda"))
+    want = torch.full((6, 4), -1.0, device="cuda")
+    want[[2, 0, 1, 3]] = scales[[0, 0, 1, 2]]
+    assert out.shape == (6, 0) and torch.equal(got, want)
