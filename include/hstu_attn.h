@@ -414,7 +414,9 @@ hstu_status_t hstu_expert_combine_bwd(const void *dout, const void *y, const int
  * the device; an expert whose offsets are not 0 <= offsets[e] <= offsets[e+1] <= rows has no rows
  * and sets HSTU_DEV_BAD_OFFSETS in *status (device int32, may be NULL, not cleared here).  Output
  * rows of no expert are left as they were.  Where offsets make experts overlap, their rows are
- * unspecified.
+ * unspecified; because that may be every second expert with all rows, sizes with (num_experts + 1) / 2
+ * * rows / 128 * ceil(output columns / 128) of about 2^31 are HSTU_ERR_UNSUPPORTED (1024 experts and
+ * 2^29 rows of up to 128 columns): their tiles could pass the kernels' counters.
  *
  * hstu_expert_proj: out [rows, d_out] = x [rows, d_in] w[e], w [num_experts, d_in, d_out], bf16;
  * silu = 1 writes SiLU of the product, and then the product itself to pre when that is not NULL.

@@ -219,6 +219,14 @@ bool proj_shape_ok(int64_t rows, int32_t experts, int32_t d_in, int32_t d_out, i
            d_in % in_step == 0 && d_in <= 65536 && d_out >= 1 && d_out % 8 == 0 && d_out <= 65536;
 }
 
+// The kernels count output tiles (of 128 x 128 at least) in 32 bits.  Experts of sound offsets share
+// `rows`; offsets that go back (rejected there, on the device) let every second one have them all.
+bool proj_tiles_ok(int64_t rows, int32_t experts, int32_t cols)
+{
+    const int64_t tiles = (int64_t)(experts + 1) / 2 * (rows / 128) + experts;
+    return tiles * ((cols + 127) / 128) <= INT32_MAX - 65536;
+}
+
 ProjArgs proj_args(const void *x, const void *w, const int64_t *offsets, int64_t rows,
                    int32_t experts, int32_t d_in, int32_t d_out, int32_t *status)
 {
@@ -723,6 +731,7 @@ hstu_status_t hstu_expert_proj(const void *x, const void *w, const int64_t *offs
     if (rows == 0) return HSTU_OK;
     if (!x || !w || !offsets || !out || !all_aligned16({x, w, offsets, out, pre}))
         return HSTU_ERR_INVALID_ARGUMENT;
+    if (!proj_tiles_ok(rows, num_experts, d_out)) return HSTU_ERR_UNSUPPORTED;
     ProjArgs a = proj_args(x, w, offsets, rows, num_experts, d_in, d_out, status);
     a.silu = silu;
     a.out = out;
@@ -742,6 +751,7 @@ hstu_status_t hstu_expert_proj_e4m3(const void *x, const float *x_scales, const 
     if (!x || !x_scales || !w || !w_scales || !offsets || !out ||
         !all_aligned16({x, x_scales, w, w_scales, offsets, out}))
         return HSTU_ERR_INVALID_ARGUMENT;
+    if (!proj_tiles_ok(rows, num_experts, d_out)) return HSTU_ERR_UNSUPPORTED;
     ProjArgs a = proj_args(x, w, offsets, rows, num_experts, d_in, d_out, status);
     a.x_scales = x_scales;
     a.w_scales = w_scales;
@@ -770,6 +780,7 @@ hstu_status_t hstu_expert_proj_bwd(const void *dout, const void *x, const void *
     if (!offsets || (rows > 0 && (!dout || (dx && !w) || (dw && !x))) ||
         !all_aligned16({dout, x, w, offsets, silu_pre, dx, dw, workspace}))
         return HSTU_ERR_INVALID_ARGUMENT;
+    if (dx && !proj_tiles_ok(rows, num_experts, d_in)) return HSTU_ERR_UNSUPPORTED;
     size_t need = 0;
     if (dw) hstu_expert_proj_bwd_workspace_size(rows, num_experts, d_in, d_out, &need);
     if (need > 0 && !workspace) return HSTU_ERR_INVALID_ARGUMENT;

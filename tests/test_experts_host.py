@@ -10,7 +10,7 @@ import torch
 from jagged_hstu_attention_02_b200 import ops
 from oracle import experts as ox
 
-INVALID, TOO_SMALL = 1, 3
+INVALID, UNSUPPORTED, TOO_SMALL = 1, 2, 3
 
 
 def _differences(f, a, step=1e-5):
@@ -266,3 +266,22 @@ def test_binding_refuses_sizes_that_the_c_abi_would_cut_to_32_bits():
     for c in calls:
         with pytest.raises(ValueError, match="2.31 or more"):
             c()
+
+
+def test_products_refuse_sizes_whose_tiles_could_pass_32_bits():
+    """Offsets 0, rows, 0, rows, ... give every second expert all rows.  The kernels reject the
+    experts between and count the others' tiles in 32 bits: 1024 experts, 2^30 rows of one column
+    of tiles would be 2^32, which is 0 tiles or places outside of the tensors."""
+    L = ops.lib()
+
+    def tiles(rows, E, cols):                          # as the kernels' table adds them up
+        return sum(-(-rows // 128) for e in range(E) if e % 2 == 0) * -(-cols // 128)
+
+    for rows, E, cols in ((2 ** 30, 1024, 8), (2 ** 22, 1024, 65536), (2 ** 31 - 1, 511, 128),
+                          (2 ** 25, 1023, 4096)):
+        assert tiles(rows, E, cols) >= 2 ** 31
+        assert L.hstu_expert_proj(_p(), _p(), _p(), rows, E, 8, cols, 0, _p(), None, None, None) == UNSUPPORTED
+        assert L.hstu_expert_proj_e4m3(_p(), _p(), _p(), _p(), _p(), rows, E, 16, cols, 0, _p(), None,
+                                       None) == UNSUPPORTED
+        assert L.hstu_expert_proj_bwd(_p(), _p(), _p(), _p(), None, rows, E, cols, 8, _p(), None, None, None,
+                                      0, None) == UNSUPPORTED
