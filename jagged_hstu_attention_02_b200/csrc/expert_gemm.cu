@@ -55,6 +55,7 @@ constexpr int kEpiWarps = 16;
 constexpr int kBand = 8;             // column tiles that the tiles in flight share
 constexpr int kMaxSorted = 256;      // experts that P_DW puts in order of their rows
 constexpr int kEThreads = 32 * (2 + kEpiWarps);
+constexpr int kMaxSmem = 232448;     // of a block (227 KB)
 
 struct EGemmArgs {
     CUtensorMap ta, ta_small, tb;
@@ -94,7 +95,7 @@ struct ELayout {
     static __host__ int stages(int experts)
     {
         int n = kMaxStages;
-        while (bytes(n, experts) > 232448) --n;
+        while (bytes(n, experts) > kMaxSmem) --n;
         return n;
     }
 };
@@ -1189,9 +1190,10 @@ bool encode(CUtensorMap *m, const void *base, bool bytes, int64_t d0, int64_t d1
            CUDA_SUCCESS;
 }
 
-// Clusters of SIZE CTAs that the device runs at a time (cached per device ordinal).
-template <int SIZE, typename K>
-int most_clusters(K kern, int smem)
+// Clusters of SIZE CTAs of Kern that the device runs at a time, with the `smem` bytes that Kern asks
+// for at most (cached per kernel and device).
+template <auto Kern, int SIZE>
+int most_clusters(int smem)
 {
     constexpr int kMaxDev = 64;
     static std::atomic<int> cache[kMaxDev];
@@ -1209,7 +1211,7 @@ int most_clusters(K kern, int smem)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&v, Kern, &cfg) != cudaSuccess || v <= 0) {
         cudaGetLastError();
         v = num_sms() / SIZE;
     }
@@ -1242,10 +1244,10 @@ cudaError_t run_egemm(const EGemmArgs &args, int64_t most_tiles, cudaStream_t st
     EGemmArgs a = args;
     a.stages = ELayout<CG>::stages(a.experts);
     const int smem = ELayout<CG>::bytes(a.stages, a.experts);
-    auto k = expert_gemm_kernel<P, CG>;
-    cudaError_t e = allow_smem<expert_gemm_kernel<P, CG>>(smem);
+    constexpr auto k = expert_gemm_kernel<P, CG>;
+    cudaError_t e = allow_smem<k>(smem);
     if (e != cudaSuccess) return e;
-    int64_t tiles = CG == 2 ? most_clusters<2>(k, smem) : num_sms();
+    int64_t tiles = CG == 2 ? most_clusters<k, 2>(kMaxSmem) : num_sms();
     if (most_tiles < tiles) tiles = most_tiles;
     if (tiles <= 0) return cudaSuccess;
     return launch_clusters(k, a, CG, tiles, smem, st);
@@ -1265,11 +1267,14 @@ cudaError_t run_parts(const EGemmArgs &args, int64_t most_tiles, cudaStream_t st
     const int64_t tile_rows = std::min<int64_t>(EBM, args.rows / args.experts);
     if (slices < 2 * PARTS || (slices - slices / PARTS) * 16 <= tile_rows || most_tiles * PARTS > num_sms())
         return cudaSuccess;
-    const int smem = ELayout<1>::c_off(kPartStages) + Joined<PARTS>::kBytes + ELayout<1>::kBarBytes +
-                     (3 * args.experts + 1) * 4 + 1024 /* alignment */;
-    auto k = expert_gemm_parts_kernel<P, PARTS>;
-    cudaError_t e = allow_smem<expert_gemm_parts_kernel<P, PARTS>>(smem);
-    if (e != cudaSuccess || most_tiles > most_clusters<PARTS>(k, smem)) return e;
+    auto bytes = [](int experts) {
+        return ELayout<1>::c_off(kPartStages) + Joined<PARTS>::kBytes + ELayout<1>::kBarBytes +
+               (3 * experts + 1) * 4 + 1024 /* alignment */;
+    };
+    const int smem = bytes(args.experts);
+    constexpr auto k = expert_gemm_parts_kernel<P, PARTS>;
+    cudaError_t e = allow_smem<k>(smem);
+    if (e != cudaSuccess || most_tiles > most_clusters<k, PARTS>(bytes(kMaxExperts))) return e;
     *done = true;
     return launch_clusters(k, args, PARTS, most_tiles, smem, st);
 }
