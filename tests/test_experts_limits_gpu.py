@@ -218,3 +218,41 @@ def test_dispatch_of_rows_without_elements_moves_their_scales():
     want = torch.full((6, 4), -1.0, device="cuda")
     want[[2, 0, 1, 3]] = scales[[0, 0, 1, 2]]
     assert out.shape == (6, 0) and torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ waits
+
+@pytest.mark.parametrize("what", ["product", "gradients"])
+@pytest.mark.parametrize("counts,K,N", [([9000, 1100], 512, 2056), ([64, 65], 4104, 136),
+                                        ([64, 65], 136, 4104), ([5000], 64, 128), ([300, 200], 512, 256)],
+                         ids=["pair", "shared", "shared gradient", "parts of the rows", "single"])
+def test_a_wait_that_runs_out_is_reported_by_every_kernel(counts, K, N, what):
+    """A planted wait that nothing satisfies runs out after a millisecond: the products on pairs of
+    blocks, with a shared contraction and from parts of the rows say so and leave the GPU usable;
+    the next call is right again."""
+    g = torch.Generator().manual_seed(K)
+    S, E = sum(counts), len(counts)
+    x, do = (torch.randn(S, n, generator=g).to(BF).cuda() for n in (K, N))
+    w = (torch.randn(E, K, N, generator=g) * K ** -0.5).to(BF).cuda()
+    off = _offsets(counts)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        if what == "product":
+            return [ops.expert_proj(x, w, off, silu=True, status=status)]
+        return ops.expert_proj_bwd(do, x, w, off, status=status)
+
+    ref = call()
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    ops.set_wait_test(2_000_000, True)
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        ops.set_wait_test(0, False)
+    assert status.item() == ops.DEV_WAIT_TIMEOUT
+    status.zero_()
+    for a, b in zip(call(), ref):
+        assert torch.equal(a, b)
+    assert status.item() == 0
