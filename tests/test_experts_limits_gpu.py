@@ -15,7 +15,7 @@ from jagged_hstu_attention_02_b200 import ops
 
 pytestmark = pytest.mark.gpu
 
-BF, F32 = torch.bfloat16, torch.float32
+BF = torch.bfloat16
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -256,3 +256,38 @@ def test_a_wait_that_runs_out_is_reported_by_every_kernel(counts, K, N, what):
     for a, b in zip(call(), ref):
         assert torch.equal(a, b)
     assert status.item() == 0
+
+
+# ------------------------------------------------------------------ the layer
+
+@pytest.mark.parametrize("T,k,E,d,ff", [(300, 2, 8, 128, 256), (77, 3, 5, 144, 136), (1, 1, 1, 64, 64)])
+def test_layer_in_8_bits_against_its_own_quantised_rows(T, k, E, d, ff):
+    """What follows the norm's 8-bit rows, from those rows and their scales in 64 bits.  Two tensors on
+    the way are rounded to bf16 and the output once more; a random product carries a relative
+    error on with a factor of at most 2, so the layer's part of the output is within 4 2^-8 of its
+    2-norm, and the output's rounding."""
+    g = torch.Generator().manual_seed(T)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g)
+
+    x, res = randn(T, d).to(BF).cuda(), (2 * randn(T, d)).to(BF).cuda()
+    nw = (1 + 0.1 * randn(d)).cuda()
+    ids = torch.randint(0, E, (T, k), generator=g).int().cuda()
+    gates = torch.softmax(randn(T, k), 1).cuda()
+    wt = randn(E, ff, d) * d ** -0.5
+    ws = wt.abs().amax(2) / 448
+    wq, ws = (wt / ws[..., None]).to(ops.F8).cuda(), ws.cuda()
+    w_out = (randn(E, ff, d) * ff ** -0.5).to(BF).cuda()
+    s = ops.expert_layer_fwd(x, res, nw, ids, gates, (wq, ws), w_out)
+    n = ops.rms_norm_rows(x, nw, res, e4m3=True)
+    rows = n.y.double() * n.scales.double()
+    part = torch.zeros(T, d, dtype=torch.float64, device="cuda")
+    for j in range(k):
+        for e in range(E):
+            t = torch.nonzero(ids[:, j] == e).squeeze(1)
+            pre = rows[t] @ (wq[e].double() * ws[e].double()[:, None]).T
+            part[t] += gates[t, j, None].double() * ((pre * torch.sigmoid(pre)) @ w_out[e].double())
+    got = s["o"].double() - s["sum"].double()
+    assert torch.equal(s["sum"], n.sum)
+    assert (got - part).norm() <= part.norm() * 4 * 2 ** -8 + s["o"].double().norm() * 2 ** -8
