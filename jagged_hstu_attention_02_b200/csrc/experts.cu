@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, combine_blocks<T, KM, true>())
 #pragma unroll
                 for (int u = 0; u < KB; ++u) {
                     const int j = j0 + u;
-                    if (a.dweights) {
+                    if (a.dweights && now.s[j] >= 0) {     // (0 times dout may be NaN)
                         float v[8];
                         f[u].get(v);
 #pragma unroll

@@ -220,6 +220,38 @@ def test_dispatch_of_rows_without_elements_moves_their_scales():
     assert out.shape == (6, 0) and torch.equal(got, want)
 
 
+# ------------------------------------------------------------------ combine
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("width", [8, 64, 100, 520, 1001, 4096])
+def test_combine_gradients_of_pairs_without_a_row_are_zero_whatever_dout_holds(width, dtype):
+    """Padding tokens' rows of dout hold NaN and infinities; neither they nor other tokens' pairs
+    without a row see them."""
+    g = torch.Generator().manual_seed(width)
+    T, k = 37, 3
+    slots = torch.randperm(T * k, generator=g).int().view(T, k)
+    slots[::4] = -1                                            # padding tokens
+    slots[1::4, 1] = -1
+    slots[2::4, 2] = T * k                                     # behind the rows
+    y = torch.randn(T * k, width, generator=g).to(dtype)
+    dout = torch.randn(T, width, generator=g).to(dtype)
+    dout[::8], dout[4::8] = float("nan"), float("inf")
+    w = torch.rand(T, k, generator=g)
+    dy, dw = ops.expert_combine_bwd(dout.cuda(), y.cuda(), slots.cuda(), w.cuda(),
+                                    grads=(torch.full_like(y, 7.0).cuda(), torch.full((T, k), 7.0).cuda()))
+    dw = dw.double().cpu()
+    live = (slots >= 0) & (slots < T * k)
+    assert (dw[~live] == 0).all()
+    rows = y.double()[slots.long().clamp(0, T * k - 1)]
+    terms = dout.double()[:, None, :] * rows
+    # a term's chain: the elements that a lane or thread adds, 5 shuffles and 8 warps
+    tol = terms.abs().sum(2) * (width / 32 + 14) * 2 ** -24
+    assert ((dw - terms.sum(2)).abs() <= tol)[live].all()
+    named = torch.zeros(T * k, dtype=torch.bool)
+    named[slots[live].long()] = True
+    assert torch.isfinite(dy.float()).all() and (dy.cpu()[~named] == 7).all()
+
+
 # ------------------------------------------------------------------ waits
 
 @pytest.mark.parametrize("what", ["product", "gradients"])
