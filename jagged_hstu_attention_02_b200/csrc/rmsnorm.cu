@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
     constexpr bool VEC = on_pieces(A), STAGED = staged_rows(A);
     constexpr int NC = chunks<W, A>();
     constexpr int kGroups = NormShape<W>::kGroups;
-    extern __shared__ __align__(128) uint8_t smem[];       // the ring, then [kGroups][width] floats
+    extern __shared__ __align__(128) uint8_t smem[];       // barriers, the ring; then [kGroups][width] floats
     __shared__ float buf[2][NormShape<W>::kThreads / 32];
     const int group = threadIdx.x / (32 * W), wg = (threadIdx.x / 32) % W;
     const bool lead = threadIdx.x % (32 * W) == 0;
@@ -559,8 +559,10 @@ __global__ void __launch_bounds__(NormShape<W>::kThreads, NormShape<W>::kBwdBloc
             }
         }
     } else {
-        // the groups' stages are done with: their memory holds the groups' parts
-        float *dws = reinterpret_cast<float *>(smem);
+        // The groups' stages are done with: their memory holds the groups' parts.  Not the barriers in
+        // front of them: a word that has been a barrier may still change after the last wait on it
+        // (parts of 5183 x 512 bf16 that lay there came out wrong in one call of six).
+        float *dws = reinterpret_cast<float *>(smem + (STAGED ? kGroups * kMaxRing * 8 : 0));
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < NC; ++c) {

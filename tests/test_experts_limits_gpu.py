@@ -178,6 +178,26 @@ def test_norm_e4m3_of_the_largest_and_smallest_values(rows, width, group):
         assert ((got - v).abs() <= tol).all(), (top, got[0, :4], v[0, :4])
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("rows,width", [(5183, 512), (9471, 464), (5980, 64), (9000, 1024), (9000, 2048), (5183, 499)])
+def test_norm_weight_gradients_of_many_rows_every_time(rows, width, dtype):
+    """More rows than groups of warps, several groups in a block: the blocks' parts meet in the memory
+    of the rings.  The same call 100 times, each within its tolerance and with the same bits."""
+    g = torch.Generator().manual_seed(rows)
+    dy, h, dsum = (torch.randn(rows, width, generator=g).to(dtype).cuda() for _ in range(3))
+    rstd = (h.double().pow(2).mean(1) + 1e-5).rsqrt().float()
+    w = (1 + 0.2 * torch.randn(width, generator=g)).cuda()
+    terms = dy.double() * h.double() * rstd.double()[:, None]
+    want, tol = terms.sum(0), (rows + 64) * 2 ** -24 * terms.abs().sum(0)
+    first = None
+    for i in range(100):
+        for d in (dsum, None):
+            dw = ops.rms_norm_rows_bwd(dy, h, rstd, w, dsum=d)[1]
+            assert ((dw.double() - want).abs() <= tol).all(), i
+            first = dw if first is None else first
+            assert torch.equal(dw, first), i
+
+
 # ------------------------------------------------------------------ sort
 
 _SORT = """
