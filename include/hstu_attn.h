@@ -337,8 +337,9 @@ hstu_status_t hstu_jagged_concat(int32_t n_parts, const void *const *values,
  *
  * hstu_rms_norm_rows_e4m3 writes y in 8 bits: q [rows, width] e4m3 (values up to 448, rounded to
  * nearest even) and scales [rows, ceil(width / group)] fp32, group = 32, 64 or 128 columns per
- * scale, or 0 for one scale per row: scale = max|y| / 448 over the group, y ~ q * scale.  A group
- * of zeros has scale 0.  NaN stays NaN.
+ * scale, or 0 for one scale per row: scale = max|y| / 448 over the group, y ~ q * scale.  Where max|y|
+ * is below about 2^-100 the scale is that of a maximum of 2^-100 (up to a factor of 2).  A group of
+ * zeros has scale 0.  NaN stays NaN.
  *
  * hstu_rms_norm_rows_bwd: with xh = h * rstd and g = dy * weight, at the stored h,
  *   dx = rstd * (g - xh * mean(g * xh)) + dsum;   dweight = sum over rows of dy * xh
@@ -377,7 +378,7 @@ hstu_status_t hstu_rms_norm_rows_bwd(const void *dy, const void *sum, const floa
  * hstu_expert_dispatch: row t of x ([tokens] rows of row_bytes bytes, any type) to row slots[t, j]
  * of out, for every j; with scales ([tokens, n_scales] fp32, NULL for none) their rows to
  * scales_out alike.  Slots outside 0..max_rows-1 are skipped; rows of out that no slot names are
- * left as they were.
+ * left as they were, one that two tokens' slots name is unspecified.
  *
  * hstu_expert_combine: out_t = residual_t + sum over j of weights[t, j] * y[slots[t, j]], summed
  * in fp32 in the order of j; y [max_rows, width], out and residual (NULL: none) [tokens, width] of
@@ -419,7 +420,8 @@ hstu_status_t hstu_expert_combine_bwd(const void *dout, const void *y, const int
  * 2^29 rows of up to 128 columns): their tiles could pass the kernels' counters.
  *
  * hstu_expert_proj: out [rows, d_out] = x [rows, d_in] w[e], w [num_experts, d_in, d_out], bf16;
- * silu = 1 writes SiLU of the product, and then the product itself to pre when that is not NULL.
+ * silu = 1 writes SiLU of the product, and then the product itself to pre when that is not NULL (SiLU
+ * within 2^-14 of its value, or 1e-17 where it goes to 0 far below zero).
  * d_in and d_out multiples of 8.
  *
  * hstu_expert_proj_e4m3: out [rows, d_out] (bf16) of e4m3 x [rows, d_in] with scales [rows] and

@@ -457,7 +457,9 @@ __device__ __forceinline__ float mul_ftz(float a, float b)
 // contraction.  a and b = 1 + exp(-.) are kept times 2^-63, so that a b stays in fp32's range up to
 // where exponents stop, at 2^126.5 (x = -87.7).  There 1 / a is 2^-126.5, which the last product
 // flushes to 0: x sigmoid(x) is 0 for any x from there down, and the other value does not notice.
-// With both far down (a b above 2^189) both are 0, an error of x sigmoid(x) below 1e-17.
+// With both far down (a b above 2^189) both are 0, an error of x sigmoid(x) below 1e-17.  (21846 rows
+// of 8 experts, 512 x 2048: 48.0 us in a burst; 47.5 without the product by 2^-63 and wrong far down,
+// 48.2 with the values clamped at -43.)
 // rx, ry: 1 - sigmoid, as exp(-x) sigmoid(x), which goes to 0 with exp(-x) (and is 0 where sigmoid
 // is: its users multiply by that).  1.f - sx would keep the reciprocal's rounding, which depends on
 // the other value, and times x = 1e6 or more that rounding is what the slope of SiLU would be.
@@ -669,7 +671,9 @@ __global__ void __launch_bounds__(kEThreads, 1) expert_gemm_kernel(const __grid_
             if (!ok) egemm_flag(a, HSTU_DEV_WAIT_TIMEOUT);
             // Every copy issued has landed before the block may exit: seen on the barriers that
             // it arrived on, or, by the other CTA of a pair, from the MMAs that have read it.
-            // (A producer that gave up has waited the limit since its last copy.)
+            // (The other CTA sees no barrier of copies that no MMA has read; where it gave up it has
+            // waited the limit since its last copy, and the leader, which it meets before it exits,
+            // drains the barriers that both CTAs' copies arrive on.)
             bool drained = true;
             for (int x = min(issued, ST); x > 0 && (rank == 0 || (ok && drained)); --x) {
                 if (--s < 0) {
@@ -1288,7 +1292,9 @@ int64_t most_row_tiles(int64_t rows, int experts, int tile)
 // Pairs of CTAs (256 x 256 tiles) read each operand half as often and reach the higher rate; single
 // CTAs (128 x 128) waste less on experts of few rows, and fill the device with fewer tiles.  32
 // experts, 1024 x 1024 bf16, single against pair: 64 rows each 18.7 against 22.8 us, 128 rows 24.6
-// against 24.9, 192 rows 30.7 against 29.7, 768 rows 84 against 64.
+// against 24.9, 192 rows 30.7 against 29.7, 768 rows 84 against 64.  The host knows the experts'
+// average alone: where one of 64 experts takes nearly all of 10000 rows, 1024 x 1024, single CTAs
+// run although pairs would be faster (52 against 47 us).
 template <int P>
 cudaError_t run_by_size(const EGemmArgs &a, int64_t rows, cudaStream_t st)
 {
@@ -1360,9 +1366,10 @@ static int64_t dw_tiles(int cg, int experts, int k, int n)
 }
 
 // Few tiles and many rows: the experts' rows are cut so that the device has work for its SMs, but
-// to no less than 256 rows on average.  The slices' fp32 sums are at most 148 tiles of 64 KB.  16384
-// rows over experts of 512 x 512, whole against parts by single CTAs against parts by pairs: two
-// experts 72, 26 and 23 us; four 51, 31 and 25; one of 32768 rows 189, 33 and 31.
+// to no less than 256 rows on average.  The slices' fp32 sums are at most 148 tiles of 64 KB, or 74 of
+// 256 KB by pairs (one expert of 512 x 512: 18.9 MB).  16384 rows over experts of 512 x 512, whole
+// against parts by single CTAs against parts by pairs: two experts 72, 26 and 23 us; four 51, 31 and
+// 25; one of 32768 rows 189, 33 and 31.
 DwPlan expert_dw_plan(int64_t rows, int experts, int k, int n)
 {
     constexpr int64_t kSms = 148;            // (the workspace's size must not depend on the device)

@@ -1,13 +1,14 @@
 // rowvec.cuh -- 256 consecutive elements of a row per warp, 8 neighbours per lane as fp32
-// registers, for kernels that walk rows of any width.
+// registers, for kernels that walk rows.
 //
 // VEC: the width is a multiple of 8, so every row starts on 16 bytes and a lane's 8 elements
-// move in 16-byte accesses.  Otherwise rows start anywhere.  A warp's 256 elements then start
-// `lead` elements in front of where they otherwise would, such that a lane's 8 lie on aligned
-// addresses of the row that is written: only a row's first and last piece are cut to single
-// elements.  Rows of the same number lie alike in every tensor of the same type; a row of
-// another number is read as the aligned pieces that cover it, and a lane puts its elements
-// together from two of them (a shuffle and a funnel shift).
+// move in 16-byte accesses (the norm, and combine of such widths).  Otherwise rows start anywhere,
+// and this is the norm's way, whose input and output rows have the same number and so lie alike in
+// every tensor of the same type.  A warp's 256 elements then start `lead` elements in front of where
+// they otherwise would, such that a lane's 8 lie on aligned addresses of the row: only its first and
+// last piece are cut to single elements.  What lies otherwise (the weights, which start on 16 bytes)
+// is read as the aligned pieces that cover it, and a lane puts its elements together from two of
+// them (a shuffle and a funnel shift).
 #pragma once
 
 #include <cuda_bf16.h>
