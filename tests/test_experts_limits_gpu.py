@@ -134,6 +134,32 @@ def test_silu_of_large_positive_values_is_the_value_and_its_slope_one(kernel, lo
     _check_slope(kernel, v)
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_silu_beside_values_that_are_not_finite(kernel):
+    """NaN and infinities stay in their own columns; NaN stays NaN, and infinity itself."""
+    v = _far(1.0, 5.0).float()
+    i = torch.arange(WIDE)
+    v[i % 8 == 2], v[i % 8 == 5], v[i % 8 == 7] = float("nan"), float("inf"), float("-inf")
+    v = v.to(BF)
+    plain = torch.isfinite(v.float())
+    want = _silu64(torch.where(plain, v, torch.zeros_like(v)))
+    x, w, off = _far_product(kernel, v, False)
+    x8, xs, w8, ws, off = _far_product(kernel, v, True)
+    for out in (ops.expert_proj(x, w, off, silu=True), ops.expert_proj_e4m3(x8, xs, w8, ws, off, silu=True)):
+        _rows_match(out[:, plain], want[plain], want[plain].abs() * (2 ** -8 + 2 ** -14) + 1e-17, "silu")
+        assert torch.isnan(out[:, v.isnan()]).all() and (out[:, v == float("inf")] == float("inf")).all()
+    counts, slices = KERNELS[kernel]
+    N, S, E = 8 if slices == 1 else slices * 64, sum(counts), len(counts)
+    dout, w = torch.zeros(S, N, device="cuda", dtype=BF), torch.zeros(E, WIDE, N, device="cuda", dtype=BF)
+    dout[:, N - 3], w[:, :, N - 3] = 1.0, 1.5
+    pre = v.cuda().expand(S, WIDE).contiguous()
+    dx = ops.expert_proj_bwd(dout, torch.zeros_like(pre), w, off, silu_pre=pre,
+                             grads=(torch.empty_like(pre), None))[0]
+    slope = 1.5 * _slope64(torch.where(plain, v, torch.zeros_like(v)))[plain]
+    _rows_match(dx[:, plain], slope, slope.abs() * 2 ** -8 + 1.5 * 1.1 * 2 ** -14, "slope")
+    assert torch.isnan(dx[:, v.isnan()]).all()
+
+
 # ------------------------------------------------------------------ norm
 
 def test_norm_without_residual_into_an_earlier_result_keeps_the_rows_themselves():
